@@ -12,6 +12,10 @@
  *   ssm_selective_state_update  one decode token per row: conv-state shift, conv,
  *                               softplus, state update in place, readout and gate
  *
+ * Beside them: the backward and replay decode of these, the scan with one decay
+ * per head (ssm_head_scan_fwd, _bwd, ssm_head_state_update) and the RMS norms
+ * around a block (ssm_residual_norm_*, ssm_gated_norm_*).
+ *
  * Conventions shared by every call
  * --------------------------------
  * - All tensor pointers are DEVICE pointers owned by the caller. The library
@@ -531,6 +535,164 @@ int ssm_selective_scan_fwd_noalloc(const void *u, const void *delta, const float
                                    const float *h0, const int32_t *cu_seqlens, int64_t S,
                                    void *y, float *h_final, int64_t tok, int64_t D, int N,
                                    ssm_dtype act_dtype, ssm_stream_t stream);
+
+/*
+ * Scan with one decay per head (linear attention with a decay), over packed
+ * sequences. Beside the per-channel scan above it is the form with a matrix
+ * state: head h of group g = h / (H / G) has a P x N state and
+ *   d_t = softplus(delta_t + dt_bias)   (or delta_t + dt_bias)
+ *   S_t = exp(d_t A) S_{t-1} + d_t u_t B_t^T
+ *   y_t = S_t C_t + Dskip u_t
+ * so B, C and u are the keys, queries and values and d_t A the log decay; the
+ * heads of a group share B and C. The cited pages have no counterpart (their
+ * mixer has a decay per channel); the conventions are ssm_selective_scan_fwd's.
+ *
+ *   u              (tok, H, P) act_dtype, u_stride elements between tokens
+ *   delta          (tok, H) act_dtype, delta_stride elements between tokens
+ *   A              (H) fp32 (negative for a decaying state)
+ *   B, C           (tok, G, N) act_dtype, bc_stride elements between tokens (both)
+ *   Dskip, dt_bias (H) fp32 or NULL (= 0)
+ *   h0             (S, H, P, N) fp32 or NULL (= zeros)
+ *   cu_seqlens, S  see the conventions above
+ *   y              (tok, H, P) act_dtype, contiguous, written; tokens outside
+ *                  every sequence are left untouched
+ *   h_final        (S, H, P, N) fp32 or NULL; may be the same buffer as h0
+ *   tok, H, P, G, N  P 1..256, N 1..128, G divides H, H * ceil(P / 64) <= 65535.
+ *                  Token strides are at least a row's width; inside a token the
+ *                  heads (groups) follow one another
+ *   workspace      >= ssm_head_scan_workspace_size() bytes, 256-byte aligned
+ *                  (NULL where that is 0); overwritten. Calls that may run at the
+ *                  same time (streams, captured graphs) need one each
+ * y must not overlap an input. Any alignment is taken; rows of bf16 that are all
+ * 16-byte aligned load faster. A decay below exp(-208) is taken as exp(-208),
+ * which is 0 in fp32. Inside one sequence a NaN or infinity in u, B, C or delta
+ * may reach every output of its own 128-token chunk, the tokens before it
+ * included, and all outputs after it; it never reaches another sequence.
+ * bf16: the products run on the tensor cores; the state, the decays and every sum
+ * are fp32.
+ */
+size_t ssm_head_scan_workspace_size(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                                    int64_t S, ssm_dtype act_dtype);
+int ssm_head_scan_fwd(const void *u, int64_t u_stride, const void *delta, int64_t delta_stride,
+                      const float *A, const void *B, const void *C, int64_t bc_stride,
+                      const float *Dskip, const float *dt_bias, int delta_softplus,
+                      const float *h0, const int32_t *cu_seqlens, int64_t S, void *y,
+                      float *h_final, int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                      ssm_dtype act_dtype, void *workspace, size_t workspace_bytes,
+                      ssm_stream_t stream);
+
+/*
+ * Backward of ssm_head_scan_fwd: gradients of sum(dy * y) + sum(dh_final *
+ * h_final). With g_t = dL/dS_t = dy_t C_t^T + exp(d_{t+1} A) g_{t+1}:
+ *   du_t = d_t g_t B_t + Dskip dy_t
+ *   dB_t = sum over the group's heads of d_t g_t^T u_t,  dC_t = the same of S_t^T dy_t
+ *   dd_t = u_t . g_t B_t + A <g_t, exp(d_t A) S_{t-1}>,  ddelta_t = dd_t softplus'
+ *   dA = sum_t d_t <g_t, exp(d_t A) S_{t-1}>,  dDskip = sum dy . u,  ddt_bias = sum ddelta
+ *   dh0 = exp(d_{t0} A) g_{t0} (first token t0; dh_final for an empty sequence)
+ * The forward's states are recomputed.
+ *   the forward's arguments, unchanged, then
+ *   dy             (tok, H, P) act_dtype, contiguous
+ *   dh_final       (S, H, P, N) fp32 or NULL (= 0)
+ *   du, ddelta, dB, dC  (tok, H, P), (tok, H), (tok, G, N) act_dtype, contiguous,
+ *                  written; tokens outside every sequence are left untouched
+ *   dA             (H) fp32, written;  dDskip, ddt_bias (H) fp32 or NULL
+ *   dh0            (S, H, P, N) fp32 or NULL, written
+ *   workspace      >= ssm_head_scan_bwd_workspace_size() bytes, 256-byte aligned
+ * Outputs must not overlap inputs. Every sum is taken in a fixed order, so results
+ * are the same bits from run to run.
+ */
+size_t ssm_head_scan_bwd_workspace_size(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                                        int64_t S, ssm_dtype act_dtype);
+int ssm_head_scan_bwd(const void *u, int64_t u_stride, const void *delta, int64_t delta_stride,
+                      const float *A, const void *B, const void *C, int64_t bc_stride,
+                      const float *Dskip, const float *dt_bias, int delta_softplus,
+                      const float *h0, const int32_t *cu_seqlens, int64_t S, const void *dy,
+                      const float *dh_final, void *du, void *ddelta, void *dB, void *dC,
+                      float *dA, float *dDskip, float *ddt_bias, float *dh0, int64_t tok,
+                      int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype act_dtype,
+                      void *workspace, size_t workspace_bytes, ssm_stream_t stream);
+
+/*
+ * One decode token per row for the scan with one decay per head: the recurrence
+ * above once, the cached state updated in place. For row b with slot
+ * s = state_indices[b] (or b when state_indices is NULL):
+ *   ssm_state[s] = exp(d A) ssm_state[s] + d x[b] B[b]^T;  y[b] = ssm_state[s] C[b] + Dskip x[b]
+ *   ssm_state      (n_slots, H, P, N) fp32, updated in place
+ *   x, dt, B, C    as u, delta, B, C of ssm_head_scan_fwd with one token per row
+ *   state_indices  (Bt) int32 or NULL (= identity, needs n_slots >= Bt); a row whose
+ *                  index is negative or >= n_slots is skipped, its y row untouched.
+ *                  Two rows naming the same slot race (undefined result).
+ *   y              (Bt, H, P) act_dtype, contiguous; must not overlap the state or
+ *                  an input (unchecked for the state)
+ * One launch, no workspace. Bt <= 65535, Bt * H < 2^31.
+ */
+int ssm_head_state_update(float *ssm_state, const void *x, int64_t x_stride, const void *dt,
+                          int64_t dt_stride, const void *B, const void *C, int64_t bc_stride,
+                          const float *A, const float *Dskip, const float *dt_bias,
+                          int delta_softplus, const int32_t *state_indices, int64_t n_slots,
+                          void *y, int64_t Bt, int64_t H, int64_t P, int64_t G, int64_t N,
+                          ssm_dtype act_dtype, ssm_stream_t stream);
+
+/* Scalars of a norm call, in HOST memory, read before the call returns. */
+typedef struct {
+    float eps;   /* >= 0, added to the mean square */
+    float alpha; /* the residual norms' scale of x; the gated norms ignore it */
+} ssm_norm_scalars;
+
+/*
+ * RMS norm after a mixer block, fused with its gate. Columns are normed in groups
+ * of `group_size` (a divisor of D; D for one group); rstd(v) = 1 / sqrt(mean(v^2) + eps):
+ *   norm_before_gate = 0:  v = x silu(z),  y = v rstd(v) weight
+ *   norm_before_gate = 1:  y = x rstd(x) weight silu(z)
+ *   x, z           (tok, D) act_dtype, x_stride / z_stride elements between rows;
+ *                  z NULL: no gate
+ *   weight         (D) fp32 or NULL (= 1)
+ *   y              (tok, D) act_dtype, contiguous; must not overlap x or z
+ * Backward, from the forward's arguments and dy (tok, D) contiguous:
+ *   dx, dz         (tok, D) act_dtype, contiguous; dz NULL allowed, ignored without z
+ *   dweight        (D) fp32 or NULL, summed over rows in a fixed order
+ *   workspace      >= ssm_norm_bwd_workspace_size(tok, D) bytes, 256-byte aligned;
+ *                  needed when dweight (or dx_scale, below) is given
+ * Norms and sums are fp32. D / group_size <= 65535.
+ */
+size_t ssm_norm_bwd_workspace_size(int64_t tok, int64_t D);
+int ssm_gated_norm_fwd(const void *x, int64_t x_stride, const void *z, int64_t z_stride,
+                       const float *weight, const ssm_norm_scalars *scalars, int norm_before_gate, void *y, int64_t tok,
+                       int64_t D, int64_t group_size, ssm_dtype act_dtype, ssm_stream_t stream);
+int ssm_gated_norm_bwd(const void *x, int64_t x_stride, const void *z, int64_t z_stride,
+                       const float *weight, const ssm_norm_scalars *scalars, int norm_before_gate, const void *dy,
+                       void *dx, void *dz, float *dweight, int64_t tok, int64_t D,
+                       int64_t group_size, ssm_dtype act_dtype, void *workspace,
+                       size_t workspace_bytes, ssm_stream_t stream);
+
+/*
+ * Residual add, residual scale and RMS norm before a mixer block:
+ *   r = residual + alpha * x_scale * x  (rounded to res_dtype),  y = r rstd(r) weight
+ *   x              (tok, D) act_dtype: the last block's output
+ *   residual       (tok, D) res_dtype or NULL (= 0): the residual stream
+ *   x_scale        (D) fp32 or NULL (= 1): a learned scale per channel; alpha: see above
+ *   residual_out   (tok, D) res_dtype or NULL: r, may be the same buffer as residual
+ *   y              (tok, D) act_dtype
+ * res_dtype is fp32, or act_dtype. y is the norm of r as it is stored. All contiguous;
+ * outputs must not overlap inputs except as stated.
+ * Backward, from r (the forward's residual_out) and dy:
+ *   dresidual_out  (tok, D) res_dtype or NULL (= 0): gradient of residual_out
+ *   dresidual      (tok, D) res_dtype or NULL: dr = norm's gradient + dresidual_out
+ *                  (may be the same buffer as dresidual_out)
+ *   dx             (tok, D) act_dtype or NULL: alpha x_scale dr
+ *   dweight        (D) fp32 or NULL;  dx_scale (D) fp32 or NULL (needs x): sum over
+ *                  rows of alpha dr x
+ */
+int ssm_residual_norm_fwd(const void *x, const void *residual, const float *x_scale,
+                          const float *weight, const ssm_norm_scalars *scalars, void *y,
+                          void *residual_out, int64_t tok, int64_t D, ssm_dtype act_dtype, ssm_dtype res_dtype,
+                          ssm_stream_t stream);
+int ssm_residual_norm_bwd(const void *r, const void *x, const float *x_scale,
+                          const float *weight, const ssm_norm_scalars *scalars, const void *dy,
+                          const void *dresidual_out, void *dx, void *dresidual, float *dweight,
+                          float *dx_scale, int64_t tok, int64_t D, ssm_dtype act_dtype,
+                          ssm_dtype res_dtype, void *workspace, size_t workspace_bytes,
+                          ssm_stream_t stream);
 
 /*
  * Measurement helpers (not part of the method; the pages have no counterpart).

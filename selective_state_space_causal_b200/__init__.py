@@ -14,14 +14,24 @@ from ._lib import (  # noqa: F401
     ssm_causal_conv1d,
     ssm_conv_scan_fwd,
     ssm_check_cu_seqlens,
+    ssm_gated_norm_bwd,
+    ssm_gated_norm_fwd,
+    ssm_head_scan_bwd,
+    ssm_head_scan_bwd_workspace_size,
+    ssm_head_scan_fwd,
+    ssm_head_scan_workspace_size,
+    ssm_head_state_update,
     ssm_last_error,
     ssm_launch_count,
+    ssm_norm_bwd_workspace_size,
     ssm_probe_rate,
     ssm_probe_sink_floats,
     ssm_device_status,
     ssm_replay_flush,
     ssm_replay_reset,
     ssm_replay_state_update,
+    ssm_residual_norm_bwd,
+    ssm_residual_norm_fwd,
     ssm_scan_bwd_workspace_size,
     ssm_scan_workspace_size,
     ssm_selective_scan_bwd,

@@ -61,6 +61,25 @@ SIGNATURES = [
     ("ssm_replay_reset", _int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]),
     ("ssm_replay_flush", _int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64,
                                 _int, _vp]),
+    ("ssm_head_scan_workspace_size", _sz, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    ("ssm_head_scan_fwd", _int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp,
+                                 _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp,
+                                 _sz, _vp]),
+    ("ssm_head_scan_bwd_workspace_size", _sz, [_i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    ("ssm_head_scan_bwd", _int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp,
+                                 _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                 _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
+    ("ssm_head_state_update", _int, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _int,
+                                     _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp]),
+    ("ssm_norm_bwd_workspace_size", _sz, [_i64, _i64]),
+    ("ssm_gated_norm_fwd", _int, [_vp, _i64, _vp, _i64, _vp, _vp, _int, _vp, _i64, _i64, _i64, _int,
+                                  _vp]),
+    ("ssm_gated_norm_bwd", _int, [_vp, _i64, _vp, _i64, _vp, _vp, _int, _vp, _vp, _vp, _vp, _i64,
+                                  _i64, _i64, _int, _vp, _sz, _vp]),
+    ("ssm_residual_norm_fwd", _int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int,
+                                     _vp]),
+    ("ssm_residual_norm_bwd", _int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                     _i64, _int, _int, _vp, _sz, _vp]),
     ("ssm_selftest_wait_timeout", _int, [_int, _vp]),
     ("ssm_probe_sink_floats", _i64, []),
     ("ssm_probe_rate", _int, [_int, _int, _int, _vp, _i64, ctypes.POINTER(ctypes.c_double), _vp]),
@@ -375,3 +394,256 @@ def ssm_conv_scan_fwd(x, conv_w, delta, A, B, C, y, conv_b=None, conv_state_in=N
         K, sdt, _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(dt_bias),
         int(bool(delta_softplus)), _ptr(h0), _ptr(cu_seqlens), S, _ptr(y), _ptr(h_final), tok, D,
         N, _dtype(x), _stream(stream)))
+
+
+class _NormScalars(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("alpha", ctypes.c_float)]
+
+
+def _token_stride(t, what: str) -> int:
+    """Elements between tokens of a (tok, ...) tensor whose tokens are contiguous rows."""
+    width = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != width:
+            raise SsmError(-1, f"{what}: the dimensions after the first must be contiguous")
+        width *= size
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _shared_stride(B, C) -> int:
+    b, c = _token_stride(B, "B"), _token_stride(C, "C")
+    if B.shape != C.shape or b != c:
+        raise SsmError(-1, "B and C must have the same shape and token stride")
+    return b
+
+
+def _same(what: str, t, dtype, shape) -> None:
+    """A contiguous tensor of this dtype and shape, or None."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise SsmError(-1, f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                           f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _head_shapes(u, delta, A, B, C, Dskip, dt_bias):
+    """(tok, H, P, G, N) after checking that the arguments agree."""
+    import torch
+
+    if u.dim() != 3 or B.dim() != 3:
+        raise SsmError(-1, "u must be (tok, H, P), B and C (tok, G, N)")
+    tok, H, P = u.shape
+    _, G, N = B.shape
+    if B.shape[0] != tok or tuple(delta.shape) != (tok, H):
+        raise SsmError(-1, "u, delta, B and C must have the same tokens, delta one column per head")
+    if not (u.dtype == delta.dtype == B.dtype == C.dtype):
+        raise SsmError(-2, "u, delta, B and C must have one dtype")
+    _same("A", A, torch.float32, (H,))
+    _same("Dskip", Dskip, torch.float32, (H,))
+    _same("dt_bias", dt_bias, torch.float32, (H,))
+    return tok, H, P, G, N
+
+
+def _act(dtype) -> int:
+    import torch
+
+    if isinstance(dtype, int):
+        return dtype
+    if dtype == torch.bfloat16:
+        return SSM_BF16
+    if dtype == torch.float32:
+        return SSM_F32
+    raise SsmError(-2, f"unsupported dtype {dtype}")
+
+
+def _on_gpu(*tensors) -> None:
+    """Every tensor on the current CUDA device: the kernels run there, on its stream."""
+    import torch
+
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise SsmError(-1, f"a tensor is on {t.device}, not on the current CUDA device")
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def ssm_head_scan_workspace_size(tok: int, H: int, P: int, G: int, N: int, S: int, dtype) -> int:
+    """Workspace bytes of ssm_head_scan_fwd; dtype is torch's or SSM_F32 / SSM_BF16."""
+    return int(lib.ssm_head_scan_workspace_size(tok, H, P, G, N, S, _act(dtype)))
+
+
+def ssm_head_scan_fwd(u, delta, A, B, C, y, Dskip=None, dt_bias=None, delta_softplus=True,
+                      h0=None, h_final=None, cu_seqlens=None, S=None, workspace=None, stream=None):
+    """Scan with one decay per head. u (tok, H, P), delta (tok, H) and B, C (tok, G, N)
+    may be slices of wider rows (tokens contiguous); y (tok, H, P) contiguous; A, Dskip,
+    dt_bias (H) fp32; h0, h_final (S, H, P, N) fp32; workspace: a device byte tensor of
+    ssm_head_scan_workspace_size() bytes."""
+    import torch
+
+    tok, H, P, G, N = _head_shapes(u, delta, A, B, C, Dskip, dt_bias)
+    if S is None:
+        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    _same("y", y, u.dtype, (tok, H, P))
+    _same("h0", h0, torch.float32, (S, H, P, N))
+    _same("h_final", h_final, torch.float32, (S, H, P, N))
+    _on_gpu(u, delta, A, B, C, y, Dskip, dt_bias, h0, h_final, cu_seqlens, workspace)
+    _check(lib.ssm_head_scan_fwd(
+        _ptr(u), _token_stride(u, "u"), _ptr(delta), _token_stride(delta, "delta"), _ptr(A), _ptr(B),
+        _ptr(C), _shared_stride(B, C), _ptr(Dskip), _ptr(dt_bias), int(bool(delta_softplus)),
+        _ptr(h0), _ptr(cu_seqlens), S, _ptr(y), _ptr(h_final), tok, H, P, G, N, _dtype(u),
+        _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def ssm_head_scan_bwd_workspace_size(tok: int, H: int, P: int, G: int, N: int, S: int, dtype) -> int:
+    """Workspace bytes of ssm_head_scan_bwd; dtype is torch's or SSM_F32 / SSM_BF16."""
+    return int(lib.ssm_head_scan_bwd_workspace_size(tok, H, P, G, N, S, _act(dtype)))
+
+
+def ssm_head_scan_bwd(u, delta, A, B, C, dy, grads, Dskip=None, dt_bias=None, delta_softplus=True,
+                      h0=None, dh_final=None, cu_seqlens=None, S=None, workspace=None,
+                      stream=None):
+    """Backward of ssm_head_scan_fwd. `grads` holds the output tensors: du (tok, H, P),
+    ddelta (tok, H), dB, dC (tok, G, N) like u's dtype, contiguous; dA (H) fp32; dDskip,
+    ddt_bias (H) fp32 or absent; dh0 (S, H, P, N) fp32 or absent."""
+    import torch
+
+    tok, H, P, G, N = _head_shapes(u, delta, A, B, C, Dskip, dt_bias)
+    if S is None:
+        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    g, f32 = grads, torch.float32
+    _same("h0", h0, f32, (S, H, P, N))
+    _same("dh_final", dh_final, f32, (S, H, P, N))
+    for name, t, dt, shape in (
+            ("dy", dy, u.dtype, (tok, H, P)), ("du", g["du"], u.dtype, (tok, H, P)),
+            ("ddelta", g["ddelta"], u.dtype, (tok, H)), ("dB", g["dB"], u.dtype, (tok, G, N)),
+            ("dC", g["dC"], u.dtype, (tok, G, N)), ("dA", g["dA"], f32, (H,)),
+            ("dDskip", g.get("dDskip"), f32, (H,)), ("ddt_bias", g.get("ddt_bias"), f32, (H,)),
+            ("dh0", g.get("dh0"), f32, (S, H, P, N))):
+        _same(name, t, dt, shape)
+        _on_gpu(t)
+    _on_gpu(u, delta, A, B, C, Dskip, dt_bias, h0, dh_final, cu_seqlens, workspace)
+    _check(lib.ssm_head_scan_bwd(
+        _ptr(u), _token_stride(u, "u"), _ptr(delta), _token_stride(delta, "delta"), _ptr(A), _ptr(B),
+        _ptr(C), _shared_stride(B, C), _ptr(Dskip), _ptr(dt_bias), int(bool(delta_softplus)),
+        _ptr(h0), _ptr(cu_seqlens), S, _ptr(dy), _ptr(dh_final), _ptr(g["du"]), _ptr(g["ddelta"]),
+        _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dA"]), _ptr(g.get("dDskip")), _ptr(g.get("ddt_bias")),
+        _ptr(g.get("dh0")), tok, H, P, G, N, _dtype(u), _ptr(workspace), _bytes(workspace),
+        _stream(stream)))
+
+
+def ssm_head_state_update(ssm_state, x, dt, B, C, y, A, Dskip=None, dt_bias=None,
+                          delta_softplus=True, state_indices=None, stream=None):
+    """One decode token per row: ssm_state (slots, H, P, N) fp32 updated in place; x (Bt, H, P),
+    dt (Bt, H), B, C (Bt, G, N) may be slices of wider rows; y (Bt, H, P) contiguous."""
+    import torch
+
+    Bt, H, P, G, N = _head_shapes(x, dt, A, B, C, Dskip, dt_bias)
+    _same("y", y, x.dtype, (Bt, H, P))
+    _same("ssm_state", ssm_state, torch.float32, (ssm_state.shape[0], H, P, N))
+    if state_indices is not None:
+        _same("state_indices", state_indices, torch.int32, (Bt,))
+    _on_gpu(ssm_state, x, dt, B, C, y, A, Dskip, dt_bias, state_indices)
+    _check(lib.ssm_head_state_update(
+        _ptr(ssm_state), _ptr(x), _token_stride(x, "x"), _ptr(dt), _token_stride(dt, "dt"), _ptr(B),
+        _ptr(C), _shared_stride(B, C), _ptr(A), _ptr(Dskip), _ptr(dt_bias),
+        int(bool(delta_softplus)), _ptr(state_indices), ssm_state.shape[0], _ptr(y), Bt, H, P, G, N,
+        _dtype(x), _stream(stream)))
+
+
+def ssm_norm_bwd_workspace_size(tok: int, D: int) -> int:
+    return int(lib.ssm_norm_bwd_workspace_size(tok, D))
+
+
+def ssm_gated_norm_fwd(x, y, weight=None, z=None, group_size=None, eps=1e-5,
+                       norm_before_gate=False, stream=None):
+    """RMS norm after a block with its silu(z) gate. x, z (tok, D) may be slices of wider
+    rows; y (tok, D) contiguous; weight (D) fp32; groups of group_size columns."""
+    import torch
+
+    tok, D = x.shape
+    _same("y", y, x.dtype, (tok, D))
+    _same("weight", weight, torch.float32, (D,))
+    if z is not None and (z.shape != x.shape or z.dtype != x.dtype):
+        raise SsmError(-1, "z must have x's shape and dtype")
+    _on_gpu(x, y, weight, z)
+    sc = _NormScalars(eps, 1.0)
+    _check(lib.ssm_gated_norm_fwd(
+        _ptr(x), _token_stride(x, "x"), _ptr(z), D if z is None else _token_stride(z, "z"),
+        _ptr(weight), ctypes.addressof(sc), int(bool(norm_before_gate)), _ptr(y), tok, D,
+        D if group_size is None else int(group_size), _dtype(x), _stream(stream)))
+
+
+def ssm_gated_norm_bwd(x, dy, grads, weight=None, z=None, group_size=None, eps=1e-5,
+                       norm_before_gate=False, workspace=None, stream=None):
+    """Backward of ssm_gated_norm_fwd. `grads` holds dx (tok, D), dz (tok, D) or absent,
+    dweight (D) fp32 or absent (which needs `workspace`)."""
+    import torch
+
+    tok, D = x.shape
+    if z is not None and (z.shape != x.shape or z.dtype != x.dtype):
+        raise SsmError(-1, "z must have x's shape and dtype")
+    _same("weight", weight, torch.float32, (D,))
+    _same("dweight", grads.get("dweight"), torch.float32, (D,))
+    for name, t in (("dy", dy), ("dx", grads["dx"]), ("dz", grads.get("dz"))):
+        _same(name, t, x.dtype, (tok, D))
+        _on_gpu(t)
+    _on_gpu(x, z, weight, grads.get("dweight"), workspace)
+    sc = _NormScalars(eps, 1.0)
+    _check(lib.ssm_gated_norm_bwd(
+        _ptr(x), _token_stride(x, "x"), _ptr(z), D if z is None else _token_stride(z, "z"),
+        _ptr(weight), ctypes.addressof(sc), int(bool(norm_before_gate)), _ptr(dy),
+        _ptr(grads["dx"]), _ptr(grads.get("dz")), _ptr(grads.get("dweight")), tok, D,
+        D if group_size is None else int(group_size), _dtype(x), _ptr(workspace),
+        _bytes(workspace), _stream(stream)))
+
+
+def ssm_residual_norm_fwd(x, y, residual=None, residual_out=None, weight=None, x_scale=None,
+                          alpha=1.0, eps=1e-5, stream=None):
+    """r = residual + alpha * x_scale * x, stored in residual_out (which may be residual);
+    y = RMS norm of r * weight. x, y (tok, D); residuals (tok, D) fp32 or x's dtype."""
+    import torch
+
+    tok, D = x.shape
+    if not x.is_contiguous():
+        raise SsmError(-1, "x must be contiguous")
+    ref = residual if residual is not None else residual_out
+    rdt = ref.dtype if ref is not None else x.dtype
+    _same("y", y, x.dtype, (tok, D))
+    _same("residual", residual, rdt, (tok, D))
+    _same("residual_out", residual_out, rdt, (tok, D))
+    _same("weight", weight, torch.float32, (D,))
+    _same("x_scale", x_scale, torch.float32, (D,))
+    _on_gpu(x, y, residual, residual_out, weight, x_scale)
+    sc = _NormScalars(eps, alpha)
+    _check(lib.ssm_residual_norm_fwd(
+        _ptr(x), _ptr(residual), _ptr(x_scale), _ptr(weight), ctypes.addressof(sc), _ptr(y),
+        _ptr(residual_out), tok, D, _dtype(x), _act(rdt), _stream(stream)))
+
+
+def ssm_residual_norm_bwd(r, dy, grads, x=None, weight=None, x_scale=None, alpha=1.0, eps=1e-5,
+                          dresidual_out=None, workspace=None, stream=None):
+    """Backward of ssm_residual_norm_fwd from r, its residual_out. `grads` holds any of dx
+    (tok, D), dresidual (tok, D) like r, dweight, dx_scale (D) fp32 (the last two need
+    `workspace`, dx_scale needs x)."""
+    import torch
+
+    tok, D = dy.shape
+    g = grads
+    for name, t, dt, shape in (
+            ("r", r, r.dtype, (tok, D)), ("dy", dy, dy.dtype, (tok, D)), ("x", x, dy.dtype, (tok, D)),
+            ("dx", g.get("dx"), dy.dtype, (tok, D)), ("dresidual", g.get("dresidual"), r.dtype, (tok, D)),
+            ("dresidual_out", dresidual_out, r.dtype, (tok, D)),
+            ("weight", weight, torch.float32, (D,)), ("x_scale", x_scale, torch.float32, (D,)),
+            ("dweight", g.get("dweight"), torch.float32, (D,)),
+            ("dx_scale", g.get("dx_scale"), torch.float32, (D,))):
+        _same(name, t, dt, shape)
+        _on_gpu(t)
+    _on_gpu(workspace)
+    sc = _NormScalars(eps, alpha)
+    _check(lib.ssm_residual_norm_bwd(
+        _ptr(r), _ptr(x), _ptr(x_scale), _ptr(weight), ctypes.addressof(sc), _ptr(dy),
+        _ptr(dresidual_out), _ptr(g.get("dx")), _ptr(g.get("dresidual")), _ptr(g.get("dweight")),
+        _ptr(g.get("dx_scale")), tok, D, _dtype(dy), _act(r.dtype), _ptr(workspace),
+        _bytes(workspace), _stream(stream)))

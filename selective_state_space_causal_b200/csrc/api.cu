@@ -145,6 +145,33 @@ int check_seqs(const char *fn, const int32_t *cu, int64_t S, int64_t tok)
     return SSM_OK;
 }
 
+bool overlap(const void *p, size_t pn, const void *q, size_t qn)
+{
+    if (!p || !q || !pn || !qn) return false;
+    const char *a = static_cast<const char *>(p), *b = static_cast<const char *>(q);
+    return a < b + qn && b < a + pn;
+}
+
+struct Region {
+    const void *p;
+    size_t n;
+};
+
+// No output may overlap an input (or another output).
+template <int NO, int NI>
+int check_apart(const char *fn, const Region (&outs)[NO], const Region (&ins)[NI])
+{
+    for (int i = 0; i < NO; ++i) {
+        for (const Region &r : ins)
+            if (overlap(outs[i].p, outs[i].n, r.p, r.n))
+                return fail(SSM_ERR_INVALID_ARGUMENT, "%s: an output overlaps an input", fn);
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+                return fail(SSM_ERR_INVALID_ARGUMENT, "%s: two outputs overlap", fn);
+    }
+    return SSM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -711,6 +738,356 @@ int ssm_probe_rate(int kind, int iters, int warps_per_sm, float *sink, int64_t s
     int launched = 0;
     cudaError_t e = ssm::launch_probe(kind, iters, warps_per_sm / 8, sink, ops,
                                       reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+// ---------------------------------------------------------------------------
+// the scan with one decay per head
+// ---------------------------------------------------------------------------
+
+// Bytes from a row-strided tensor's first element to past its last.
+static size_t span_bytes(int64_t rows, int64_t stride, int64_t width, size_t es)
+{
+    return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * es : 0;
+}
+
+static bool head_sizes_ok(int64_t H, int64_t P, int64_t G, int64_t N)
+{
+    return H >= 1 && P >= 1 && P <= 256 && N >= 1 && N <= 128 && G >= 1 && G <= H && H % G == 0 &&
+           H <= 65535 && H * ((P + 63) / 64) <= 65535;
+}
+
+static int check_head_sizes(const char *fn, int64_t H, int64_t P, int64_t G, int64_t N)
+{
+    if (head_sizes_ok(H, P, G, N)) return SSM_OK;
+    return fail(SSM_ERR_INVALID_ARGUMENT,
+                "%s: bad sizes (H=%lld, P=%lld, G=%lld, N=%lld): P 1..256, N 1..128, G divides H, "
+                "H * ceil(P / 64) <= 65535",
+                fn, (long long)H, (long long)P, (long long)G, (long long)N);
+}
+
+static int check_stride(const char *fn, const char *what, int64_t rows, int64_t stride, int64_t width)
+{
+    if (stride >= width && stride <= ((int64_t)1 << 40)) return SSM_OK;
+    if (rows <= 1) return SSM_OK;  // a single row has no next one
+    return fail(SSM_ERR_INVALID_ARGUMENT, "%s: the token stride of %s is %lld, a row has %lld", fn,
+                what, (long long)stride, (long long)width);
+}
+
+static bool head_ws_args_ok(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N, int64_t S,
+                            ssm_dtype act_dtype)
+{
+    return valid_dtype(act_dtype) && head_sizes_ok(H, P, G, N) && tok >= 0 &&
+           tok <= (int64_t)INT32_MAX && S >= 1 && S <= 65535;
+}
+
+size_t ssm_head_scan_workspace_size(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                                    int64_t S, ssm_dtype act_dtype)
+{
+    if (!head_ws_args_ok(tok, H, P, G, N, S, act_dtype)) return 0;
+    return ssm::head_scan_workspace_bytes(tok, H, P, G, N, S, dt(act_dtype));
+}
+
+size_t ssm_head_scan_bwd_workspace_size(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                                        int64_t S, ssm_dtype act_dtype)
+{
+    if (!head_ws_args_ok(tok, H, P, G, N, S, act_dtype)) return 0;
+    return ssm::head_scan_bwd_workspace_bytes(tok, H, P, G, N, S, dt(act_dtype));
+}
+
+static int check_workspace(const char *fn, const void *workspace, size_t bytes, size_t need)
+{
+    if (need == 0) return SSM_OK;
+    if (!workspace || bytes < need)
+        return fail(SSM_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+                    workspace ? bytes : (size_t)0, need);
+    if (!aligned(workspace, 256))
+        return fail(SSM_ERR_MISALIGNED, "%s: workspace must be 256-byte aligned", fn);
+    return SSM_OK;
+}
+
+// Checks that the forward and the backward share.
+static int check_head_scan(const char *fn, const ssm::HeadScanArgs &a, ssm_dtype act_dtype)
+{
+    if (!valid_dtype(act_dtype)) return fail(SSM_ERR_UNSUPPORTED_DTYPE, "%s: unknown dtype", fn);
+    if (int r = check_head_sizes(fn, a.H, a.P, a.G, a.N)) return r;
+    if (int r = check_seqs(fn, a.cu, a.S, a.tok)) return r;
+    if (int r = check_stride(fn, "u", a.tok, a.u_stride, a.H * a.P)) return r;
+    if (int r = check_stride(fn, "delta", a.tok, a.delta_stride, a.H)) return r;
+    if (int r = check_stride(fn, "B and C", a.tok, a.bc_stride, a.G * a.N)) return r;
+    if (!a.A) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: A is NULL", fn);
+    if (a.tok > 0 && (!a.u || !a.delta || !a.B || !a.C))
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: u, delta, B and C are required", fn);
+    const size_t es = esize(act_dtype);
+    const void *acts[] = {a.u, a.delta, a.B, a.C, a.y, a.dy, a.du, a.ddelta, a.dB, a.dC};
+    for (const void *q : acts)
+        if (!aligned(q, es))
+            return fail(SSM_ERR_MISALIGNED, "%s: a pointer is not aligned to its element size", fn);
+    const void *f32s[] = {a.A, a.Dskip, a.dt_bias, a.h0, a.h_final, a.dh_final, a.dA, a.dDskip,
+                          a.ddt_bias, a.dh0};
+    for (const void *q : f32s)
+        if (!aligned(q, 4)) return fail(SSM_ERR_MISALIGNED, "%s: an fp32 pointer is misaligned", fn);
+    return SSM_OK;
+}
+
+int ssm_head_scan_fwd(const void *u, int64_t u_stride, const void *delta, int64_t delta_stride,
+                      const float *A, const void *B, const void *C, int64_t bc_stride,
+                      const float *Dskip, const float *dt_bias, int delta_softplus,
+                      const float *h0, const int32_t *cu_seqlens, int64_t S, void *y,
+                      float *h_final, int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                      ssm_dtype act_dtype, void *workspace, size_t workspace_bytes,
+                      ssm_stream_t stream)
+{
+    const char *fn = "ssm_head_scan_fwd";
+    ssm::HeadScanArgs a{u, delta, A, B, C, u_stride, delta_stride, bc_stride, Dskip, dt_bias,
+                        delta_softplus, h0, cu_seqlens, S, tok, H, P, G, N, dt(act_dtype),
+                        workspace, y, h_final};
+    if (int r = check_head_scan(fn, a, act_dtype)) return r;
+    if (tok > 0 && !y) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: y is NULL", fn);
+    const size_t need = ssm_head_scan_workspace_size(tok, H, P, G, N, S, act_dtype);
+    if (int r = check_workspace(fn, workspace, workspace_bytes, need)) return r;
+    const size_t es = esize(act_dtype), bc = span_bytes(tok, bc_stride, G * N, es);
+    const size_t state = (size_t)S * H * P * N * 4;
+    const Region outs[] = {{y, (size_t)tok * H * P * es}, {workspace, need}};
+    const Region ins[] = {{u, span_bytes(tok, u_stride, H * P, es)},
+                          {delta, span_bytes(tok, delta_stride, H, es)}, {B, bc}, {C, bc},
+                          {h0, state}, {h_final, state}};
+    if (int r = check_apart(fn, outs, ins)) return r;
+    if (h_final != h0 && overlap(h_final, state, h0, state))
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: h_final overlaps h0 without being it", fn);
+    int launched = 0;
+    cudaError_t e = ssm::launch_head_scan(a, reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+int ssm_head_scan_bwd(const void *u, int64_t u_stride, const void *delta, int64_t delta_stride,
+                      const float *A, const void *B, const void *C, int64_t bc_stride,
+                      const float *Dskip, const float *dt_bias, int delta_softplus,
+                      const float *h0, const int32_t *cu_seqlens, int64_t S, const void *dy,
+                      const float *dh_final, void *du, void *ddelta, void *dB, void *dC,
+                      float *dA, float *dDskip, float *ddt_bias, float *dh0, int64_t tok,
+                      int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype act_dtype,
+                      void *workspace, size_t workspace_bytes, ssm_stream_t stream)
+{
+    const char *fn = "ssm_head_scan_bwd";
+    ssm::HeadScanArgs a{u, delta, A, B, C, u_stride, delta_stride, bc_stride, Dskip, dt_bias,
+                        delta_softplus, h0, cu_seqlens, S, tok, H, P, G, N, dt(act_dtype),
+                        workspace, nullptr, nullptr, dy, dh_final, du, ddelta, dB, dC, dA, dDskip,
+                        ddt_bias, dh0};
+    if (int r = check_head_scan(fn, a, act_dtype)) return r;
+    if (!dA) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: dA is NULL", fn);
+    if (tok > 0 && (!dy || !du || !ddelta || !dB || !dC))
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: dy, du, ddelta, dB and dC are required", fn);
+    const size_t need = ssm_head_scan_bwd_workspace_size(tok, H, P, G, N, S, act_dtype);
+    if (int r = check_workspace(fn, workspace, workspace_bytes, need)) return r;
+    const size_t es = esize(act_dtype), bc = span_bytes(tok, bc_stride, G * N, es);
+    const size_t rows = (size_t)tok * H * P * es, state = (size_t)S * H * P * N * 4;
+    const size_t heads = (size_t)H * 4, dbc = (size_t)tok * G * N * es;
+    const Region outs[] = {{du, rows}, {ddelta, (size_t)tok * H * es}, {dB, dbc}, {dC, dbc},
+                           {dA, heads}, {dDskip, heads}, {ddt_bias, heads}, {dh0, state},
+                           {workspace, need}};
+    const Region ins[] = {{u, span_bytes(tok, u_stride, H * P, es)},
+                          {delta, span_bytes(tok, delta_stride, H, es)}, {B, bc}, {C, bc},
+                          {dy, rows}, {h0, state}, {dh_final, state}, {A, heads},
+                          {Dskip, heads}, {dt_bias, heads}};
+    if (int r = check_apart(fn, outs, ins)) return r;
+    int launched = 0;
+    cudaError_t e = ssm::launch_head_scan_bwd(a, reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+int ssm_head_state_update(float *ssm_state, const void *x, int64_t x_stride, const void *dt_,
+                          int64_t dt_stride, const void *B, const void *C, int64_t bc_stride,
+                          const float *A, const float *Dskip, const float *dt_bias,
+                          int delta_softplus, const int32_t *state_indices, int64_t n_slots,
+                          void *y, int64_t Bt, int64_t H, int64_t P, int64_t G, int64_t N,
+                          ssm_dtype act_dtype, ssm_stream_t stream)
+{
+    const char *fn = "ssm_head_state_update";
+    if (!valid_dtype(act_dtype)) return fail(SSM_ERR_UNSUPPORTED_DTYPE, "%s: unknown dtype", fn);
+    if (int r = check_head_sizes(fn, H, P, G, N)) return r;
+    if (Bt < 0 || Bt > 65535 || Bt * H > (int64_t)INT32_MAX || n_slots < 0)
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: bad sizes (Bt=%lld, H=%lld, n_slots=%lld)", fn,
+                    (long long)Bt, (long long)H, (long long)n_slots);
+    if (!state_indices && n_slots < Bt)
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: identity slots need n_slots >= Bt", fn);
+    if (int r = check_stride(fn, "x", Bt, x_stride, H * P)) return r;
+    if (int r = check_stride(fn, "dt", Bt, dt_stride, H)) return r;
+    if (int r = check_stride(fn, "B and C", Bt, bc_stride, G * N)) return r;
+    if (Bt > 0 && (!ssm_state || !x || !dt_ || !B || !C || !A || !y))
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: a required pointer is NULL", fn);
+    const size_t es = esize(act_dtype);
+    const void *acts[] = {x, dt_, B, C, y};
+    for (const void *q : acts)
+        if (!aligned(q, es))
+            return fail(SSM_ERR_MISALIGNED, "%s: a pointer is not aligned to its element size", fn);
+    const void *w32[] = {ssm_state, A, Dskip, dt_bias, state_indices};
+    for (const void *q : w32)
+        if (!aligned(q, 4)) return fail(SSM_ERR_MISALIGNED, "%s: a 32-bit pointer is misaligned", fn);
+    const size_t bc = span_bytes(Bt, bc_stride, G * N, es);
+    const Region outs[] = {{y, (size_t)Bt * H * P * es}};
+    const Region ins[] = {{x, span_bytes(Bt, x_stride, H * P, es)},
+                          {dt_, span_bytes(Bt, dt_stride, H, es)}, {B, bc}, {C, bc}};
+    if (int r = check_apart(fn, outs, ins)) return r;
+    ssm::HeadStepArgs a{ssm_state, x, dt_, B, C, x_stride, dt_stride, bc_stride, A, Dskip, dt_bias,
+                        delta_softplus, state_indices, n_slots, y, Bt, H, P, G, N, dt(act_dtype)};
+    int launched = 0;
+    cudaError_t e = ssm::launch_head_step(a, reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+// ---------------------------------------------------------------------------
+// norms around a block
+// ---------------------------------------------------------------------------
+size_t ssm_norm_bwd_workspace_size(int64_t tok, int64_t D)
+{
+    if (tok < 0 || D < 1 || D > (int64_t)INT32_MAX) return 0;
+    return ssm::norm_bwd_workspace_bytes(tok, D);
+}
+
+static int check_norm_sizes(const char *fn, int64_t tok, int64_t D, int64_t group,
+                            const ssm_norm_scalars *scalars)
+{
+    if (!scalars) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: scalars is NULL", fn);
+    if (tok < 0 || tok > (int64_t)INT32_MAX || D < 1 || D > (1 << 24))
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: bad sizes (tok=%lld, D=%lld)", fn,
+                    (long long)tok, (long long)D);
+    if (group < 1 || D % group != 0 || D / group > 65535)
+        return fail(SSM_ERR_INVALID_ARGUMENT,
+                    "%s: group_size (%lld) must divide D (%lld), in at most 65535 groups", fn,
+                    (long long)group, (long long)D);
+    if (!(scalars->eps >= 0.0f)) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: eps must be >= 0", fn);
+    return SSM_OK;
+}
+
+static int check_norm_aligned(const char *fn, const ssm::NormArgs &n, size_t es, size_t rs)
+{
+    const void *acts[] = {n.x, n.z, n.y, n.dy, n.dx, n.dz};
+    for (const void *q : acts)
+        if (!aligned(q, es))
+            return fail(SSM_ERR_MISALIGNED, "%s: a pointer is not aligned to its element size", fn);
+    const void *ress[] = {n.residual, n.residual_out, n.x_res, n.dres_out, n.dres};
+    for (const void *q : ress)
+        if (!aligned(q, rs))
+            return fail(SSM_ERR_MISALIGNED, "%s: a residual pointer is not aligned to its element size", fn);
+    const void *f32s[] = {n.weight, n.x_scale, n.dweight, n.dscale};
+    for (const void *q : f32s)
+        if (!aligned(q, 4)) return fail(SSM_ERR_MISALIGNED, "%s: an fp32 pointer is misaligned", fn);
+    return SSM_OK;
+}
+
+int ssm_gated_norm_fwd(const void *x, int64_t x_stride, const void *z, int64_t z_stride,
+                       const float *weight, const ssm_norm_scalars *scalars, int norm_before_gate, void *y, int64_t tok,
+                       int64_t D, int64_t group_size, ssm_dtype act_dtype, ssm_stream_t stream)
+{
+    const char *fn = "ssm_gated_norm_fwd";
+    if (!valid_dtype(act_dtype)) return fail(SSM_ERR_UNSUPPORTED_DTYPE, "%s: unknown dtype", fn);
+    if (int r = check_norm_sizes(fn, tok, D, group_size, scalars)) return r;
+    if (int r = check_stride(fn, "x", tok, x_stride, D)) return r;
+    if (z)
+        if (int r = check_stride(fn, "z", tok, z_stride, D)) return r;
+    if (tok > 0 && (!x || !y)) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: x and y are required", fn);
+    ssm::NormArgs n{true, x, z, nullptr, x_stride, z_stride, weight, nullptr, 1.0f, scalars->eps,
+                    norm_before_gate, y, nullptr, tok, D, group_size, dt(act_dtype), dt(act_dtype)};
+    const size_t es = esize(act_dtype);
+    if (int r = check_norm_aligned(fn, n, es, es)) return r;
+    const Region outs[] = {{y, (size_t)tok * D * es}};
+    const Region ins[] = {{x, span_bytes(tok, x_stride, D, es)}, {z, span_bytes(tok, z_stride, D, es)},
+                          {weight, (size_t)D * 4}};
+    if (int r = check_apart(fn, outs, ins)) return r;
+    int launched = 0;
+    cudaError_t e = ssm::launch_norm_fwd(n, reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+int ssm_gated_norm_bwd(const void *x, int64_t x_stride, const void *z, int64_t z_stride,
+                       const float *weight, const ssm_norm_scalars *scalars, int norm_before_gate, const void *dy,
+                       void *dx, void *dz, float *dweight, int64_t tok, int64_t D,
+                       int64_t group_size, ssm_dtype act_dtype, void *workspace,
+                       size_t workspace_bytes, ssm_stream_t stream)
+{
+    const char *fn = "ssm_gated_norm_bwd";
+    if (!valid_dtype(act_dtype)) return fail(SSM_ERR_UNSUPPORTED_DTYPE, "%s: unknown dtype", fn);
+    if (int r = check_norm_sizes(fn, tok, D, group_size, scalars)) return r;
+    if (int r = check_stride(fn, "x", tok, x_stride, D)) return r;
+    if (z)
+        if (int r = check_stride(fn, "z", tok, z_stride, D)) return r;
+    if (tok > 0 && (!x || !dy || !dx))
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: x, dy and dx are required", fn);
+    ssm::NormArgs n{true, x, z, nullptr, x_stride, z_stride, weight, nullptr, 1.0f, scalars->eps,
+                    norm_before_gate, nullptr, nullptr, tok, D, group_size, dt(act_dtype),
+                    dt(act_dtype), dy, nullptr, nullptr, dx, z ? dz : nullptr, nullptr, dweight,
+                    nullptr, static_cast<float *>(workspace)};
+    const size_t es = esize(act_dtype);
+    if (int r = check_norm_aligned(fn, n, es, es)) return r;
+    const size_t need = dweight ? ssm_norm_bwd_workspace_size(tok, D) : 0;
+    if (int r = check_workspace(fn, workspace, workspace_bytes, need)) return r;
+    const size_t rows = (size_t)tok * D * es, cols = (size_t)D * 4;
+    const Region outs[] = {{dx, rows}, {n.dz, rows}, {dweight, cols}, {workspace, need}};
+    const Region ins[] = {{x, span_bytes(tok, x_stride, D, es)}, {z, span_bytes(tok, z_stride, D, es)},
+                          {dy, rows}, {weight, cols}};
+    if (int r = check_apart(fn, outs, ins)) return r;
+    int launched = 0;
+    cudaError_t e = ssm::launch_norm_bwd(n, reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+int ssm_residual_norm_fwd(const void *x, const void *residual, const float *x_scale,
+                          const float *weight, const ssm_norm_scalars *scalars, void *y,
+                          void *residual_out, int64_t tok, int64_t D, ssm_dtype act_dtype, ssm_dtype res_dtype,
+                          ssm_stream_t stream)
+{
+    const char *fn = "ssm_residual_norm_fwd";
+    if (!valid_dtype(act_dtype) || !valid_dtype(res_dtype) ||
+        (res_dtype != SSM_F32 && res_dtype != act_dtype))
+        return fail(SSM_ERR_UNSUPPORTED_DTYPE, "%s: res_dtype must be fp32 or act_dtype", fn);
+    if (int r = check_norm_sizes(fn, tok, D, D, scalars)) return r;
+    if (tok > 0 && (!x || !y)) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: x and y are required", fn);
+    ssm::NormArgs n{false, x, nullptr, residual, D, 0, weight, x_scale, scalars->alpha, scalars->eps, 0, y,
+                    residual_out, tok, D, D, dt(act_dtype), dt(res_dtype)};
+    const size_t es = esize(act_dtype), rs = esize(res_dtype);
+    if (int r = check_norm_aligned(fn, n, es, rs)) return r;
+    const size_t rows = (size_t)tok * D * es, stream_bytes = (size_t)tok * D * rs, cols = (size_t)D * 4;
+    const Region outs[] = {{y, rows}, {residual_out, stream_bytes}};
+    const Region ins[] = {{x, rows}, {residual_out == residual ? nullptr : residual, stream_bytes},
+                          {weight, cols}, {x_scale, cols}};
+    if (int r = check_apart(fn, outs, ins)) return r;
+    int launched = 0;
+    cudaError_t e = ssm::launch_norm_fwd(n, reinterpret_cast<cudaStream_t>(stream), &launched);
+    return finish(e, launched, fn);
+}
+
+int ssm_residual_norm_bwd(const void *r, const void *x, const float *x_scale,
+                          const float *weight, const ssm_norm_scalars *scalars, const void *dy,
+                          const void *dresidual_out, void *dx, void *dresidual, float *dweight,
+                          float *dx_scale, int64_t tok, int64_t D, ssm_dtype act_dtype,
+                          ssm_dtype res_dtype, void *workspace, size_t workspace_bytes,
+                          ssm_stream_t stream)
+{
+    const char *fn = "ssm_residual_norm_bwd";
+    if (!valid_dtype(act_dtype) || !valid_dtype(res_dtype) ||
+        (res_dtype != SSM_F32 && res_dtype != act_dtype))
+        return fail(SSM_ERR_UNSUPPORTED_DTYPE, "%s: res_dtype must be fp32 or act_dtype", fn);
+    if (int c = check_norm_sizes(fn, tok, D, D, scalars)) return c;
+    if (tok > 0 && (!r || !dy)) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: r and dy are required", fn);
+    if (tok > 0 && dx_scale && !x)
+        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: dx_scale needs x", fn);
+    ssm::NormArgs n{false, x, nullptr, nullptr, D, 0, weight, x_scale, scalars->alpha, scalars->eps, 0, nullptr,
+                    nullptr, tok, D, D, dt(act_dtype), dt(res_dtype), dy, r, dresidual_out, dx,
+                    nullptr, dresidual, dweight, dx_scale, static_cast<float *>(workspace)};
+    const size_t es = esize(act_dtype), rs = esize(res_dtype);
+    if (int c = check_norm_aligned(fn, n, es, rs)) return c;
+    const size_t need = dweight || dx_scale ? ssm_norm_bwd_workspace_size(tok, D) : 0;
+    if (int c = check_workspace(fn, workspace, workspace_bytes, need)) return c;
+    const size_t rows = (size_t)tok * D * es, stream_bytes = (size_t)tok * D * rs, cols = (size_t)D * 4;
+    const Region outs[] = {{dx, rows}, {dresidual, stream_bytes}, {dweight, cols}, {dx_scale, cols},
+                           {workspace, need}};
+    const Region ins[] = {{r, stream_bytes}, {x, rows}, {dy, rows},
+                          {dresidual == dresidual_out ? nullptr : dresidual_out, stream_bytes},
+                          {weight, cols}, {x_scale, cols}};
+    if (int c = check_apart(fn, outs, ins)) return c;
+    int launched = 0;
+    cudaError_t e = ssm::launch_norm_bwd(n, reinterpret_cast<cudaStream_t>(stream), &launched);
     return finish(e, launched, fn);
 }
 

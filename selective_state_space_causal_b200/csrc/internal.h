@@ -64,6 +64,73 @@ struct DecodeArgs {
     DType dtype, conv_dtype;
 };
 
+// The scan with one decay per head; strides are elements between tokens.
+struct HeadScanArgs {
+    const void *u, *delta;
+    const float *A;
+    const void *B, *C;
+    int64_t u_stride, delta_stride, bc_stride;
+    const float *Dskip, *dt_bias;
+    int delta_softplus;
+    const float *h0;
+    const int32_t *cu;
+    int64_t S;
+    int64_t tok, H, P, G, N;
+    DType dtype;
+    void *workspace;
+    // forward
+    void *y = nullptr;
+    float *h_final = nullptr;
+    // backward
+    const void *dy = nullptr;
+    const float *dh_final = nullptr;
+    void *du = nullptr, *ddelta = nullptr, *dB = nullptr, *dC = nullptr;
+    float *dA = nullptr, *dDskip = nullptr, *ddt_bias = nullptr, *dh0 = nullptr;
+};
+
+struct HeadStepArgs {
+    float *state;
+    const void *x, *dt, *B, *C;
+    int64_t x_stride, dt_stride, bc_stride;
+    const float *A, *Dskip, *dt_bias;
+    int delta_softplus;
+    const int32_t *idx;
+    int64_t n_slots;
+    void *y;
+    int64_t Bt, H, P, G, N;
+    DType dtype;
+};
+
+// Norms around a mixer block. Gated: x and z with row strides, groups of
+// `group` columns. Residual: r = residual + alpha * x_scale * x, group = D.
+struct NormArgs {
+    bool gated;
+    const void *x, *z, *residual;
+    int64_t x_stride, z_stride;
+    const float *weight, *x_scale;
+    float alpha, eps;
+    int norm_before_gate;
+    void *y, *residual_out;
+    int64_t tok, D, group;
+    DType dtype, res_dtype;
+    // backward (x_res: the residual stream that the forward stored)
+    const void *dy = nullptr, *x_res = nullptr, *dres_out = nullptr;
+    void *dx = nullptr, *dz = nullptr, *dres = nullptr;
+    float *dweight = nullptr, *dscale = nullptr;
+    float *partials = nullptr;
+};
+
+size_t head_scan_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N, int64_t S,
+                                 DType dtype);
+size_t head_scan_bwd_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
+                                     int64_t S, DType dtype);
+cudaError_t launch_head_scan(const HeadScanArgs &a, cudaStream_t stream, int *launches);
+cudaError_t launch_head_scan_bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches);
+cudaError_t launch_head_step(const HeadStepArgs &a, cudaStream_t stream, int *launches);
+size_t norm_bwd_workspace_bytes(int64_t tok, int64_t D);
+cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t stream, int *launches);
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t stream, int *launches);
+
 // Each returns cudaSuccess or the launch error.
 cudaError_t launch_conv1d(const ConvArgs &a, cudaStream_t stream, int *launches);
 cudaError_t launch_scan(const ScanArgs &a, cudaStream_t stream, int *launches);

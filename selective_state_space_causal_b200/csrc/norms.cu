@@ -1,0 +1,549 @@
+// norms.cu -- RMS norms around a mixer block, fused with the gate and the residual.
+//
+//   gated (after the block):  v = x silu(z), y = v rstd(v) w  per group of columns,
+//                             or, with the norm before the gate, y = x rstd(x) w silu(z)
+//   residual (before it):     r = residual + alpha x_scale x (as stored), y = r rstd(r) w
+//
+// Backward, with vh = v rstd, dh = dy w (times the gate when it comes after the norm):
+//   dv = rstd (dh - vh mean(dh vh)),  dw = sum over rows of dy vh (times the gate).
+//
+// All four are bound by memory: every input is read once and every output written
+// once, because a team of threads (a warp for groups up to 256 vectors, a block
+// beyond) keeps its row in registers between the sum and the scaling. Vectors are 16
+// bytes. Rows that are not 16-byte aligned, or longer than the registers hold, go to
+// kernels that read the row twice (the second time from cache).
+#include "common.cuh"
+#include "internal.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kParts = 1184;  // most partial rows of a weight gradient (8 per SM of 148)
+
+struct Args {
+    const void *x, *z, *residual, *dy, *xres, *dro;
+    int64_t xs, zs;
+    const float *w, *scale;
+    float alpha, eps;
+    void *y, *ro, *dx, *dz, *dres;
+    float *part;
+    int64_t tok;
+    int D, group;
+    bool has_dw, has_ds;
+};
+
+__device__ __forceinline__ float sigmoid_of(float z, float) { return 1.0f / (1.0f + expf(-z)); }
+__device__ __forceinline__ float sigmoid_of(float z, __nv_bfloat16)
+{
+    return __fdividef(1.0f, 1.0f + __expf(-z));  // inf in the denominator gives 0
+}
+
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float *sm)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (TEAM > 32) {
+        __syncthreads();  // sm may still be read from the call before
+        if ((threadIdx.x & 31) == 0) sm[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TEAM / 32; ++i) v += sm[i];
+    }
+    return v;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_f(const T *p, float (&v)[V])
+{
+    if constexpr (V * sizeof(T) == 32) {
+        float a[V / 2], b[V / 2];
+        load_vec<T, V / 2>(p, a);
+        load_vec<T, V / 2>(p + V / 2, b);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) { v[i] = a[i]; v[V / 2 + i] = b[i]; }
+    } else {
+        load_vec<T, V>(p, v);
+    }
+}
+
+// read-write data (a residual stream updated in place): no read-only cache
+template <typename T, int V>
+__device__ __forceinline__ void load_rw(const T *p, float (&v)[V])
+{
+    static_assert((V * sizeof(T)) % 16 == 0, "16-byte vectors");
+#pragma unroll
+    for (int q = 0; q < (int)(V * sizeof(T) / 16); ++q) {
+        const uint4 raw = reinterpret_cast<const uint4 *>(p)[q];
+        const T *e = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+        for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[q * (16 / sizeof(T)) + i] = to_f32(e[i]);
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_f(T *p, const float (&v)[V])
+{
+    if constexpr (V * sizeof(T) == 32) {
+        float a[V / 2], b[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) { a[i] = v[i]; b[i] = v[V / 2 + i]; }
+        store_vec<T, V / 2>(p, a);
+        store_vec<T, V / 2>(p + V / 2, b);
+    } else {
+        store_vec<T, V>(p, v);
+    }
+}
+
+// V elements per vector: 8 for bf16 activations, 4 for fp32.
+template <typename T> struct VecOf { static constexpr int v = 16 / sizeof(T); };
+
+// MODE 0: x only; 1: gate then norm; 2: norm then gate; 3: residual.
+template <typename T, typename R, int MODE, int TEAM, int K>
+__global__ void __launch_bounds__(256) norm_fwd_kernel(Args a)
+{
+    constexpr int V = VecOf<T>::v;
+    __shared__ float sm[8];
+    const int l = threadIdx.x % TEAM;
+    const int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM;
+    if (TEAM == 32 && row >= a.tok) return;  // a block-wide team always has a row
+    const int gs = a.group, c0 = blockIdx.y * gs;
+    const T *x = static_cast<const T *>(a.x) + row * a.xs + c0;
+    const T *z = MODE == 1 || MODE == 2 ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr;
+    const R *res = MODE == 3 && a.residual ? static_cast<const R *>(a.residual) + row * a.D : nullptr;
+    R *ro = MODE == 3 && a.ro ? static_cast<R *>(a.ro) + row * a.D : nullptr;
+    float v[K][V], gate[MODE == 2 ? K : 1][V], ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (l + TEAM * k) * V;
+        if (c >= gs) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
+            continue;
+        }
+        load_f<T, V>(x + c, v[k]);
+        if (MODE == 1 || MODE == 2) {
+            float zv[V];
+            load_f<T, V>(z + c, zv);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float gv = zv[i] * sigmoid_of(zv[i], T());
+                if (MODE == 1) v[k][i] *= gv;
+                else gate[k][i] = gv;
+            }
+        }
+        if (MODE == 3) {
+            float rv[V] = {}, sc[V];
+            if (res) load_rw<R, V>(res + c, rv);
+            if (a.scale) load_f<float, V>(a.scale + c, sc);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float s = a.scale ? a.alpha * sc[i] : a.alpha;
+                // the norm is of the stream as it is stored, which the backward reads
+                v[k][i] = to_f32(from_f32<R>(fmaf(s, v[k][i], rv[i])));
+            }
+            if (ro) store_f<R, V>(ro + c, v[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+    }
+    const float rstd = 1.0f / sqrtf(team_sum<TEAM>(ss, sm) / (float)gs + a.eps);
+    T *y = static_cast<T *>(a.y) + row * a.D + c0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (l + TEAM * k) * V;
+        if (c >= gs) continue;
+        float wv[V];
+        if (a.w) load_f<float, V>(a.w + c0 + c, wv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[k][i] *= rstd;
+            if (a.w) v[k][i] *= wv[i];
+            if (MODE == 2) v[k][i] *= gate[k][i];
+        }
+        store_f<T, V>(y + c, v[k]);
+    }
+}
+
+// Teams walk rows with a stride; thread l keeps the weight-gradient sums of its columns.
+template <typename T, typename R, int MODE, int TEAM, int K>
+__global__ void __launch_bounds__(256) norm_bwd_kernel(Args a)
+{
+    constexpr int V = VecOf<T>::v;
+    __shared__ float sm[8];
+    const int l = threadIdx.x % TEAM;
+    const int64_t team = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM;
+    const int64_t teams = (int64_t)gridDim.x * (256 / TEAM);
+    const int gs = a.group, c0 = blockIdx.y * gs;
+    float dw[K][V] = {}, ds[MODE == 3 ? K : 1][V] = {};
+    for (int64_t row = team; row < a.tok; row += teams) {
+        const T *x = a.x ? static_cast<const T *>(a.x) + row * a.xs + c0 : nullptr;
+        const T *z = MODE == 1 || MODE == 2 ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr;
+        const T *dyp = static_cast<const T *>(a.dy) + row * a.D + c0;
+        const R *xr = MODE == 3 ? static_cast<const R *>(a.xres) + row * a.D : nullptr;
+        // v: the normed value; q: dy (times the gate for MODE 2)
+        float v[K][V], q[K][V], ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (l + TEAM * k) * V;
+            if (c >= gs) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[k][i] = q[k][i] = 0.0f;
+                continue;
+            }
+            if (MODE == 3) load_f<R, V>(xr + c, v[k]);
+            else load_f<T, V>(x + c, v[k]);
+            load_f<T, V>(dyp + c, q[k]);
+            float wv[V];
+            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
+            if (MODE == 1 || MODE == 2) {
+                float zv[V];
+                load_f<T, V>(z + c, zv);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float gv = zv[i] * sigmoid_of(zv[i], T());
+                    if (MODE == 1) v[k][i] *= gv;
+                    else q[k][i] *= gv;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                ss = fmaf(v[k][i], v[k][i], ss);
+                dot = fmaf(a.w ? q[k][i] * wv[i] : q[k][i], v[k][i], dot);
+            }
+        }
+        ss = team_sum<TEAM>(ss, sm);
+        dot = team_sum<TEAM>(dot, sm);
+        const float rstd = 1.0f / sqrtf(ss / (float)gs + a.eps);
+        const float m = dot * rstd * rstd / (float)gs;  // mean(dh vh) rstd, for vh = v rstd
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (l + TEAM * k) * V;
+            if (c >= gs) continue;
+            float wv[V], out[V];
+            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
+            else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) wv[i] = 1.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dw[k][i] = fmaf(q[k][i], v[k][i] * rstd, dw[k][i]);
+                out[i] = rstd * (q[k][i] * wv[i] - v[k][i] * m);  // dv
+            }
+            if (MODE == 0) {
+                store_f<T, V>(static_cast<T *>(a.dx) + row * a.D + c0 + c, out);
+            } else if (MODE == 3) {
+                float sc[V], o2[V];
+                if (a.dro) {
+                    load_rw<R, V>(static_cast<const R *>(a.dro) + row * a.D + c, o2);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) out[i] += o2[i];
+                }
+                if (a.dres) store_f<R, V>(static_cast<R *>(a.dres) + row * a.D + c, out);
+                if (a.scale) load_f<float, V>(a.scale + c, sc);
+                if (a.has_ds) {
+                    float xv[V];
+                    load_f<T, V>(x + c, xv);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) ds[k][i] = fmaf(a.alpha * out[i], xv[i], ds[k][i]);
+                }
+                if (a.dx) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o2[i] = out[i] * (a.scale ? a.alpha * sc[i] : a.alpha);
+                    store_f<T, V>(static_cast<T *>(a.dx) + row * a.D + c, o2);
+                }
+            } else {
+                // x and z again, from cache: keeping them would cost 2 K V registers
+                float xv[V], zv[V], yv[V], dxv[V], dzv[V];
+                load_f<T, V>(x + c, xv);
+                load_f<T, V>(z + c, zv);
+                if (MODE == 2) load_f<T, V>(dyp + c, yv);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float sg = sigmoid_of(zv[i], T());
+                    const float dsilu = sg * fmaf(zv[i], 1.0f - sg, 1.0f);
+                    if (MODE == 1) {
+                        dxv[i] = out[i] * (zv[i] * sg);
+                        dzv[i] = out[i] * xv[i] * dsilu;
+                    } else {
+                        dxv[i] = out[i];
+                        dzv[i] = yv[i] * (xv[i] * rstd) * wv[i] * dsilu;
+                    }
+                }
+                store_f<T, V>(static_cast<T *>(a.dx) + row * a.D + c0 + c, dxv);
+                if (a.dz) store_f<T, V>(static_cast<T *>(a.dz) + row * a.D + c0 + c, dzv);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (l + TEAM * k) * V;
+        if (c >= gs) continue;
+        if (a.has_dw) store_f<float, V>(a.part + team * a.D + c0 + c, dw[k]);
+        if (MODE == 3 && a.has_ds) store_f<float, V>(a.part + (teams + team) * a.D + c0 + c, ds[MODE == 3 ? k : 0]);
+    }
+}
+
+// Any size and alignment: a block per row (and group), elements one by one, the row read twice.
+template <typename T, typename R, int MODE>
+__device__ __forceinline__ float normed(const Args &a, int64_t row, int c0, int c, float &gate)
+{
+    float v;
+    gate = 1.0f;
+    if (MODE == 3) {
+        v = to_f32(static_cast<const R *>(a.xres)[row * a.D + c]);
+    } else {
+        v = to_f32(static_cast<const T *>(a.x)[row * a.xs + c0 + c]);
+        if (MODE != 0) {
+            const float zv = to_f32(static_cast<const T *>(a.z)[row * a.zs + c0 + c]);
+            gate = zv * sigmoid_of(zv, T());
+            if (MODE == 1) v *= gate;
+        }
+    }
+    return v;
+}
+
+template <typename T, typename R, int MODE>
+__global__ void __launch_bounds__(256) norm_fwd_any_kernel(Args a)
+{
+    __shared__ float sm[8];
+    const int64_t row = blockIdx.x;
+    const int gs = a.group, c0 = blockIdx.y * gs;
+    const T *x = static_cast<const T *>(a.x) + row * a.xs + c0;
+    const R *res = MODE == 3 && a.residual ? static_cast<const R *>(a.residual) + row * a.D : nullptr;
+    R *ro = MODE == 3 && a.ro ? static_cast<R *>(a.ro) + row * a.D : nullptr;
+    T *y = static_cast<T *>(a.y) + row * a.D + c0;
+    // a stream updated in place is not read again after it was written
+    auto stream = [&](int c) {
+        if (res == ro && res && ro) return to_f32(ro[c]);
+        const float s = a.scale ? a.alpha * a.scale[c] : a.alpha;
+        return to_f32(from_f32<R>(fmaf(s, to_f32(x[c]), res ? to_f32(res[c]) : 0.0f)));
+    };
+    float ss = 0.0f, gate;
+    for (int c = threadIdx.x; c < gs; c += 256) {
+        float v;
+        if (MODE == 3) {
+            const float s = a.scale ? a.alpha * a.scale[c] : a.alpha;
+            const R r = from_f32<R>(fmaf(s, to_f32(x[c]), res ? to_f32(res[c]) : 0.0f));
+            if (ro) ro[c] = r;
+            v = to_f32(r);
+        } else {
+            v = normed<T, R, MODE>(a, row, c0, c, gate);
+        }
+        ss = fmaf(v, v, ss);
+    }
+    const float rstd = 1.0f / sqrtf(team_sum<256>(ss, sm) / (float)gs + a.eps);
+    for (int c = threadIdx.x; c < gs; c += 256) {
+        gate = 1.0f;
+        float v = MODE == 3 ? stream(c) : normed<T, R, MODE>(a, row, c0, c, gate);
+        v *= rstd;
+        if (a.w) v *= a.w[c0 + c];
+        if (MODE == 2) v *= gate;
+        y[c] = from_f32<T>(v);
+    }
+}
+
+// Thread c sums over its block's rows into the block's partial row in memory.
+template <typename T, typename R, int MODE>
+__global__ void __launch_bounds__(256) norm_bwd_any_kernel(Args a)
+{
+    __shared__ float sm[8];
+    const int gs = a.group, c0 = blockIdx.y * gs;
+    const int64_t team = blockIdx.x, teams = gridDim.x;
+    float *pw = a.part + team * a.D + c0, *ps = a.part + (teams + team) * a.D + c0;
+    for (int c = threadIdx.x; c < gs; c += 256) {
+        if (a.has_dw) pw[c] = 0.0f;
+        if (a.has_ds) ps[c] = 0.0f;
+    }
+    for (int64_t row = team; row < a.tok; row += teams) {
+        const T *dyp = static_cast<const T *>(a.dy) + row * a.D + c0;
+        float ss = 0.0f, dot = 0.0f, gate;
+        for (int c = threadIdx.x; c < gs; c += 256) {
+            const float v = normed<T, R, MODE>(a, row, c0, c, gate);
+            float q = to_f32(dyp[c]) * (a.w ? a.w[c0 + c] : 1.0f);
+            if (MODE == 2) q *= gate;
+            ss = fmaf(v, v, ss);
+            dot = fmaf(q, v, dot);
+        }
+        ss = team_sum<256>(ss, sm);
+        dot = team_sum<256>(dot, sm);
+        const float rstd = 1.0f / sqrtf(ss / (float)gs + a.eps);
+        const float m = dot * rstd * rstd / (float)gs;
+        for (int c = threadIdx.x; c < gs; c += 256) {
+            const float v = normed<T, R, MODE>(a, row, c0, c, gate);
+            const float w = a.w ? a.w[c0 + c] : 1.0f, dyv = to_f32(dyp[c]);
+            const float q = MODE == 2 ? dyv * gate : dyv;
+            if (a.has_dw) pw[c] = fmaf(q, v * rstd, pw[c]);
+            float dv = rstd * (q * w - v * m);
+            const int64_t at = row * a.D + c0 + c;
+            if (MODE == 3) {
+                if (a.dro) dv += to_f32(static_cast<const R *>(a.dro)[at]);
+                const float s = a.scale ? a.alpha * a.scale[c] : a.alpha;
+                if (a.has_ds)
+                    ps[c] = fmaf(a.alpha * dv, to_f32(static_cast<const T *>(a.x)[row * a.xs + c]), ps[c]);
+                if (a.dres) static_cast<R *>(a.dres)[at] = from_f32<R>(dv);
+                if (a.dx) static_cast<T *>(a.dx)[at] = from_f32<T>(s * dv);
+            } else if (MODE == 0) {
+                static_cast<T *>(a.dx)[at] = from_f32<T>(dv);
+            } else {
+                const float xv = to_f32(static_cast<const T *>(a.x)[row * a.xs + c0 + c]);
+                const float zv = to_f32(static_cast<const T *>(a.z)[row * a.zs + c0 + c]);
+                const float sg = sigmoid_of(zv, T());
+                const float dsilu = sg * fmaf(zv, 1.0f - sg, 1.0f);
+                static_cast<T *>(a.dx)[at] = from_f32<T>(MODE == 1 ? dv * (zv * sg) : dv);
+                if (a.dz)
+                    static_cast<T *>(a.dz)[at] =
+                        from_f32<T>((MODE == 1 ? dv * xv : dyv * (xv * rstd) * w) * dsilu);
+            }
+        }
+    }
+}
+
+// out[c] = sum over partial rows, in a fixed order: 32 columns by 8 strides of rows per block.
+__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *part, int parts, int D, float *out)
+{
+    __shared__ double sm[8][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, r0 = threadIdx.x / 32;
+    double s = 0.0;
+    if (c < D)
+        for (int r = r0; r < parts; r += 8) s += part[(int64_t)r * D + c];
+    sm[r0][threadIdx.x % 32] = s;
+    __syncthreads();
+    if (r0 == 0 && c < D) {
+        for (int i = 1; i < 8; ++i) s += sm[i][threadIdx.x];
+        out[c] = (float)s;
+    }
+}
+
+bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <typename T, typename R, int MODE>
+cudaError_t fwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st)
+{
+    constexpr int V = VecOf<T>::v;
+    const unsigned groups = (unsigned)(n.D / n.group);
+    const int nv = (int)(n.group / V);
+    const dim3 warps((unsigned)((n.tok + 7) / 8), groups), rows((unsigned)n.tok, groups);
+    if (!vec || nv > 2048) norm_fwd_any_kernel<T, R, MODE><<<rows, 256, 0, st>>>(a);
+    else if (nv <= 32) norm_fwd_kernel<T, R, MODE, 32, 1><<<warps, 256, 0, st>>>(a);
+    else if (nv <= 64) norm_fwd_kernel<T, R, MODE, 32, 2><<<warps, 256, 0, st>>>(a);
+    else if (nv <= 256) norm_fwd_kernel<T, R, MODE, 256, 1><<<rows, 256, 0, st>>>(a);
+    else if (nv <= 512) norm_fwd_kernel<T, R, MODE, 256, 2><<<rows, 256, 0, st>>>(a);
+    else if (nv <= 1024) norm_fwd_kernel<T, R, MODE, 256, 4><<<rows, 256, 0, st>>>(a);
+    else norm_fwd_kernel<T, R, MODE, 256, 8><<<rows, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, typename R, int MODE>
+cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int *parts)
+{
+    constexpr int V = VecOf<T>::v;
+    const unsigned groups = (unsigned)(n.D / n.group);
+    const int nv = (int)(n.group / V);
+    const bool team32 = vec && nv <= 64;
+    // enough blocks to fill the GPU over all groups, few enough partial rows
+    int64_t blocks = team32 ? (n.tok + 7) / 8 : n.tok;
+    const int64_t most = team32 ? kParts / 8 : kParts / 2;
+    if (blocks > most) blocks = most;
+    const dim3 grid((unsigned)blocks, groups);
+    *parts = (int)(team32 ? blocks * 8 : blocks);
+    if (!vec || nv > 1024) norm_bwd_any_kernel<T, R, MODE><<<grid, 256, 0, st>>>(a);
+    else if (nv <= 32) norm_bwd_kernel<T, R, MODE, 32, 1><<<grid, 256, 0, st>>>(a);
+    else if (nv <= 64) norm_bwd_kernel<T, R, MODE, 32, 2><<<grid, 256, 0, st>>>(a);
+    else if (nv <= 256) norm_bwd_kernel<T, R, MODE, 256, 1><<<grid, 256, 0, st>>>(a);
+    else if (nv <= 512) norm_bwd_kernel<T, R, MODE, 256, 2><<<grid, 256, 0, st>>>(a);
+    else norm_bwd_kernel<T, R, MODE, 256, 4><<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+Args common(const NormArgs &n)
+{
+    Args a;
+    a.x = n.x; a.z = n.z; a.residual = n.residual;
+    a.dy = n.dy; a.xres = n.x_res; a.dro = n.dres_out;
+    a.xs = n.x_stride; a.zs = n.z_stride;
+    a.w = n.weight; a.scale = n.x_scale;
+    a.alpha = n.alpha; a.eps = n.eps;
+    a.y = n.y; a.ro = n.residual_out; a.dx = n.dx; a.dz = n.dz; a.dres = n.dres;
+    a.part = n.partials;
+    a.tok = n.tok; a.D = (int)n.D; a.group = (int)n.group;
+    a.has_dw = n.dweight != nullptr;
+    a.has_ds = n.dscale != nullptr;
+    return a;
+}
+
+// Every pointer 16-byte aligned, strides and the group multiples of a vector.
+bool vectors(const NormArgs &n, int V)
+{
+    const void *ps[] = {n.x, n.z, n.residual, n.weight, n.x_scale, n.y, n.residual_out,
+                        n.dy, n.x_res, n.dres_out, n.dx, n.dz, n.dres};
+    for (const void *p : ps)
+        if (!al16(p)) return false;
+    return n.group % V == 0 && n.x_stride % V == 0 && (!n.z || n.z_stride % V == 0);
+}
+
+template <typename F>
+cudaError_t by_type(const NormArgs &n, F f)
+{
+    using bf = __nv_bfloat16;
+    const bool b = n.dtype == DType::BF16, rb = n.res_dtype == DType::BF16;
+    if (n.gated) return b ? f(bf(), bf()) : f(float(), float());
+    if (b) return rb ? f(bf(), bf()) : f(bf(), float());
+    return f(float(), float());
+}
+
+}  // namespace
+
+size_t norm_bwd_workspace_bytes(int64_t tok, int64_t D)
+{
+    (void)tok;
+    return (size_t)2 * kParts * D * sizeof(float);
+}
+
+cudaError_t launch_norm_fwd(const NormArgs &n, cudaStream_t st, int *launches)
+{
+    if (n.tok == 0) return cudaSuccess;
+    const Args a = common(n);
+    ++*launches;
+    return by_type(n, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        const bool vec = vectors(n, VecOf<T>::v);
+        if (!n.gated) return fwd<T, R, 3>(n, a, vec, st);
+        if (!n.z) return fwd<T, R, 0>(n, a, vec, st);
+        return n.norm_before_gate ? fwd<T, R, 2>(n, a, vec, st) : fwd<T, R, 1>(n, a, vec, st);
+    });
+}
+
+cudaError_t launch_norm_bwd(const NormArgs &n, cudaStream_t st, int *launches)
+{
+    const Args a = common(n);
+    int parts = 0;
+    if (n.tok > 0) {
+        ++*launches;
+        const cudaError_t e = by_type(n, [&](auto t, auto r) {
+            using T = decltype(t);
+            using R = decltype(r);
+            const bool vec = vectors(n, VecOf<T>::v);
+            if (!n.gated) return bwd<T, R, 3>(n, a, vec, st, &parts);
+            if (!n.z) return bwd<T, R, 0>(n, a, vec, st, &parts);
+            return n.norm_before_gate ? bwd<T, R, 2>(n, a, vec, st, &parts)
+                                      : bwd<T, R, 1>(n, a, vec, st, &parts);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    const unsigned blocks = (unsigned)((n.D + 31) / 32);
+    float *outs[2] = {n.dweight, n.dscale};
+    for (int i = 0; i < 2; ++i) {
+        if (!outs[i]) continue;
+        norm_reduce_kernel<<<blocks, 256, 0, st>>>(n.partials + (size_t)i * parts * n.D, parts,
+                                                   (int)n.D, outs[i]);
+        ++*launches;
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace ssm
