@@ -8,7 +8,7 @@
 //   du = M^T dy + d_s e^{cQ-c_s} dS B_s + D dy,
 //   dC = sum_h (dM L d) B + e^{c_t} S0^T dy,  dB = sum_h (dM L d)^T C + d_s e^{cQ-c_s} dS^T u,
 // with c the running sum of d_t A inside the chunk.
-#include "head_scan.cuh"
+#include "head_mma.cuh"
 
 namespace ssm {
 namespace {
@@ -559,7 +559,10 @@ cudaError_t bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 size_t head_scan_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N, int64_t S,
                                  DType dtype)
 {
-    return 0;
+    if (dtype != DType::BF16) return 0;
+    HeadScanArgs a{};
+    a.S = S; a.tok = tok; a.H = H; a.P = P; a.G = G; a.N = N;
+    return hm::forward_bytes(hm::dims_of(a));
 }
 
 size_t head_scan_bwd_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
@@ -571,7 +574,7 @@ size_t head_scan_bwd_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t 
 
 cudaError_t launch_head_scan(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 {
-    return a.dtype == DType::BF16 ? fwd<__nv_bfloat16>(a, stream, launches)
+    return a.dtype == DType::BF16 ? hm::launch_forward(a, stream, launches)
                                   : fwd<float>(a, stream, launches);
 }
 

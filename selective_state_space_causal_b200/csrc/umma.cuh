@@ -1,0 +1,140 @@
+// umma.cuh -- tcgen05 matrix instructions on bf16 tiles in shared and tensor memory.
+//
+// Operand tiles are panels of R rows x 64 bf16, 128 bytes a row, rows in order, the
+// 16-byte pieces of row r permuted by piece ^ (r & 7) (the 128-byte swizzle), each
+// panel 1024-byte aligned. The same panel serves both ways:
+//   K-major   rows are the operand's M (or N) index, the 64 columns its K index;
+//   MN-major  rows are the K index, the 64 columns the M (or N) index; 128 columns
+//             are two panels, one `panel` stride apart.
+// Accumulators are 128 lanes x N fp32 columns of tensor memory, one row a lane.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "tma.cuh"
+
+namespace ssm {
+namespace umma {
+
+constexpr uint32_t kPanel = 128 * 128;  // bytes of a 128-row panel
+
+// Byte offset of 16-byte piece `c` of row r in a panel.
+__device__ __forceinline__ uint32_t piece(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// Shared-memory descriptor: 128-byte swizzle, strides in bytes.
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead, uint32_t stride)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lead >> 4) << 16) |
+           ((uint64_t)(stride >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// K-major: 8 rows (1024 bytes) from one group to the next; a step of 16 along K is 32 bytes.
+__device__ __forceinline__ uint64_t desc_k(uint32_t panel, int k16)
+{
+    return desc(panel + k16 * 32, 16, 1024);
+}
+// MN-major: 8 rows along K are 1024 bytes, the next 64 columns one panel away; 16 rows a step.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t panel, int k16, uint32_t next)
+{
+    return desc(panel + k16 * 2048, next, 1024);
+}
+
+// Instruction descriptor: bf16 x bf16 -> fp32, M = 128.
+__device__ __forceinline__ constexpr uint32_t idesc(int N, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// D (+)= A B, operands in shared memory. One thread.
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u) : "memory");
+}
+
+// The same with A in tensor memory: row a lane, two bf16 of K a column.
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+        :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u) : "memory");
+}
+
+// The barrier completes once every matrix instruction this thread issued before has.
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(saddr(bar)) : "memory");
+}
+
+// One warp: allocate / free `cols` (a power of two >= 32) columns of tensor memory.
+__device__ __forceinline__ void alloc(uint32_t *slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(saddr(slot)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(cols));
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Address of this warp's lanes: a warp reaches lanes 32 (warp % 4) .. + 31.
+__device__ __forceinline__ uint32_t lanes(uint32_t base, int warp) { return base + ((uint32_t)(warp & 3) << 21); }
+
+// 32 columns of this thread's lane. The values are there after wait_ld.
+__device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Two fp32 to a bf16 pair, lo in the low half.
+__device__ __forceinline__ uint32_t pack(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// 16 bytes global -> shared; without `in`, zeros and no read.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+}  // namespace umma
+}  // namespace ssm
