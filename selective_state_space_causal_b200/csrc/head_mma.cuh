@@ -3,9 +3,13 @@
 //
 // Chunks have 128 tokens, the M of the matrix instructions. A state is worked on in
 // panels of 64 rows (head, 64 of its P rows); rows and columns beyond P and N are
-// zeros. Workspace tables hold, per (chunk slot, head), the steps d_t and the running
-// sum of d_t A log2(e) inside the chunk, the latter in 64 bits: it reaches hundreds,
-// and what is used are small differences of it.
+// zeros. Workspace tables hold what a chunk's decays are needed as, per (chunk slot,
+// head) and token t: with c_t the running sum of d_t A log2(e) inside the chunk, made in
+// 64 bits because it reaches hundreds and small differences of it are used, and r_i
+// its value before 32-token block i,
+//   d      d_t                      l      c_t - r_{block of t}
+//   ec     2^{c_t}                  wf     d_t 2^{c_127 - c_t}
+//   col    d_t 2^{r_i - c_t} for blocks i = 1..3 and t < 32 i (192 values)
 #pragma once
 
 #include "head_scan.cuh"
@@ -40,6 +44,12 @@ __device__ __forceinline__ PanelRef panel_of(const Dims &z, int g, int pi)
     return r;
 }
 
+// Tables of one (chunk slot, head), in floats.
+constexpr int kTabD = 0, kTabL = kC, kTabEc = 2 * kC, kTabCol = 3 * kC, kTabWf = 3 * kC + 192;
+constexpr int kTab = 4 * kC + 192;
+constexpr int kTabOut = kTabWf;  // what the outputs need comes first
+__host__ __device__ constexpr int col_at(int i) { return kTabCol + (i == 1 ? 0 : i == 2 ? 32 : 96); }
+
 // Eight bf16 of a row as 16 bytes, elements from `n` on as zeros.
 __device__ __forceinline__ uint4 read8(const bf16 *p, int n)
 {
@@ -66,28 +76,50 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr)
     return v;
 }
 
-// One 16-byte piece (n of its 8 elements inside the tensor) into shared memory; vec:
-// sources are 16-byte aligned and n is 0 or 8.
-__device__ __forceinline__ void load_piece(uint32_t dst, const bf16 *src, int n, bool vec)
+// Tokens [0, len) of a slice with `cols` columns as panels of 128 rows x 64, zeros
+// elsewhere. VEC: rows are 16-byte aligned and `cols` a multiple of 8.
+template <int COLS, int THREADS, bool VEC>
+__device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t stride, int len,
+                                          int cols, int tid)
 {
-    if (vec) umma::cp16(dst, src, n > 0);
-    else sts16(dst, n > 0 ? read8(src, n) : make_uint4(0, 0, 0, 0));
+    constexpr int PIECES = COLS / 8, ROWS = THREADS / PIECES;  // rows of one pass
+    static_assert(THREADS % PIECES == 0 && kC % ROWS == 0, "whole passes");
+    const int r0 = tid / PIECES, c = tid % PIECES;
+    const int n = min(8, cols - 8 * c);
+    const bf16 *q = src + r0 * stride + 8 * c;
+    const int64_t step = ROWS * stride;
+    const uint32_t at = dst + (c / 8) * umma::kPanel;
+#pragma unroll
+    for (int i = 0; i < kC / ROWS; ++i) {
+        const int r = r0 + ROWS * i;
+        const bool in = r < len && n > 0;
+        const uint32_t to = at + umma::piece(r, c % 8);
+        if (VEC) umma::cp16(to, in ? q : src, in);
+        else sts16(to, in ? read8(q, n) : make_uint4(0, 0, 0, 0));
+        q += step;
+    }
 }
 
-// Tokens [t0, t0 + len) of a (tok, cols) slice as panels of 128 rows x 64, zeros elsewhere.
-template <int COLS, int THREADS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t stride, int len,
-                                          int cols, bool vec, int tid)
+// The same by one warp, without copies in flight afterwards.
+template <int COLS>
+__device__ __forceinline__ void load_tile_warp(uint32_t dst, const bf16 *src, int64_t stride, int len,
+                                               int cols, int lane)
 {
     constexpr int PIECES = COLS / 8;
-    static_assert(kC * PIECES % THREADS == 0, "whole passes");
-#pragma unroll
-    for (int i = 0; i < kC * PIECES / THREADS; ++i) {
-        const int x = tid + THREADS * i, r = x / PIECES, c = x % PIECES;
-        const int n = r < len ? min(8, cols - 8 * c) : 0;
-        load_piece(dst + (c / 8) * umma::kPanel + umma::piece(r, c % 8),
-                   n > 0 ? src + r * stride + 8 * c : src, n, vec);
+    for (int i = lane; i < kC * PIECES; i += 32) {
+        const int r = i / PIECES, c = i % PIECES, n = min(8, cols - 8 * c);
+        const bool in = r < len && n > 0;
+        sts16(dst + (c / 8) * umma::kPanel + umma::piece(r, c % 8),
+              in ? read8(src + r * stride + 8 * c, n) : make_uint4(0, 0, 0, 0));
     }
+}
+
+// Rows [len, 128) of `panels` panels become zeros (a tile copy brought the next sequence's).
+__device__ __forceinline__ void zero_tail(uint32_t dst, int panels, int len, int tid, int threads)
+{
+    const int n = (kC - len) * 8;
+    for (int i = tid; i < n * panels; i += threads)
+        sts16(dst + (i / n) * umma::kPanel + len * 128 + (i % n) * 16, make_uint4(0, 0, 0, 0));
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads)
@@ -95,14 +127,14 @@ __device__ __forceinline__ void bar_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
-// A state mark: per panel and plane, NPAD / 8 pieces x 64 rows x 8 bf16, so that both
-// a thread per row (writing) and a copy piece by piece (reading) touch whole lines.
+// A state mark: per panel and plane, NPAD / 8 pieces x 64 rows x 8 bf16: a thread per
+// row writes whole lines, and a plain copy of it is a matrix operand without swizzle.
 template <int NPAD>
 constexpr int64_t kMark = (int64_t)64 * NPAD;  // elements of one plane
 
 // Scratch that one call needs, carved from the workspace in this order.
 struct Layout {
-    size_t c, d, seg, segdec, marks, total;
+    size_t tab, seg, segdec, marks, total;
 };
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -113,24 +145,25 @@ struct StateArgs {
     int64_t x_stride;
     const bf16 *b;  // B, or C in the reverse walk
     int64_t b_stride;
-    const double *c;
-    const float *d;
+    const float *tab;
     const float *init;  // (S, H, P, N) or nullptr
     float *final_;      // (S, H, P, N) or nullptr
     bf16 *marks;        // state before each chunk in walking order
     int64_t span;       // tokens of a segment (a multiple of kC)
     float *seg;         // split walks: (segment slot, panel, NPAD / 4, 64, 4) end, then start states
-    double *segdec;     // (segment slot, head): the segment's decay, log2
-    bool x_vec, b_vec;
+    float *segdec;      // (segment slot, head): the segment's decay
+    int segment;        // 0: whole sequences; 1, 2: the passes of a split walk
 };
 
 // Steps and running decays of every chunk.
-cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, double *c, float *d,
-                          cudaStream_t stream, int *launches);
+cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, cudaStream_t stream,
+                          int *launches);
 // The states before every chunk (forward) or the gradients of the states after every
 // chunk (reverse), `planes` bf16 planes each.
-cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, cudaStream_t stream,
-                          int *launches);
+cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, bool vec,
+                          cudaStream_t stream, int *launches);
+// Workspace of the tables and of one walk's segments and marks.
+Layout layout_of(const Dims &z, int planes, int64_t span, bool split);
 Dims dims_of(const HeadScanArgs &a);
 // Tokens per segment of the walk, and whether walks are split.
 int64_t segment_span(const Dims &z, bool *split);

@@ -7,7 +7,7 @@
 // with rows p (both panels), B = b. w x is split into three bf16 planes (24 bits), so the
 // state keeps fp32 accuracy; b is bf16 as given. The products of different chunks are
 // independent: only S' = e S + delta runs chunk after chunk, in registers, while the
-// next product is under way.
+// next products are under way.
 #include "head_mma.cuh"
 
 namespace ssm {
@@ -20,7 +20,7 @@ namespace {
 // One block per (chunk slot, 32 heads).
 __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *delta, int64_t stride,
                                                          const float *A, const float *bias,
-                                                         int softplus, double *c, float *d)
+                                                         int softplus, float *tab)
 {
     __shared__ float sd[kC][33];
     const int64_t slot = blockIdx.x;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
     if (ck.len == 0) return;
     const int h = h0 + lane;
     const float bs = bias && h < z.H ? bias[h] : 0.0f;
-#pragma unroll
+#pragma unroll 4
     for (int t = warp; t < kC; t += 8) {
         float v = 0.0f;
         if (t < ck.len && h < z.H) v = head_step(to_f32(delta[(ck.start + t) * stride + h]) + bs, softplus);
@@ -55,17 +55,39 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
             const double v = __shfl_up_sync(0xffffffffu, pre, o);
             if (lane >= o) pre += v;
         }
+        const double last = __shfl_sync(0xffffffffu, pre, 31);
+        const double r1 = __shfl_sync(0xffffffffu, pre, 7), r2 = __shfl_sync(0xffffffffu, pre, 15),
+                     r3 = __shfl_sync(0xffffffffu, pre, 23);
         pre -= sum;
-        const int64_t at = (slot * z.H + h0 + i) * kC + 4 * lane;
+        const int blk = lane / 8;
+        const double r = blk == 0 ? 0.0 : blk == 1 ? r1 : blk == 2 ? r2 : r3;
+        float lv[4], ev[4], wv[4], c1[4], c2[4], c3[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) run[j] += pre;
-        *reinterpret_cast<double2 *>(c + at) = make_double2(run[0], run[1]);
-        *reinterpret_cast<double2 *>(c + at + 2) = make_double2(run[2], run[3]);
-        *reinterpret_cast<float4 *>(d + at) = make_float4(dv[0], dv[1], dv[2], dv[3]);
+        for (int j = 0; j < 4; ++j) {
+            const double c = pre + run[j];
+            lv[j] = (float)(c - r);
+            ev[j] = ex2_approx((float)c);
+            wv[j] = dv[j] * ex2_approx((float)(last - c));
+            c1[j] = dv[j] * ex2_approx((float)(r1 - c));
+            c2[j] = dv[j] * ex2_approx((float)(r2 - c));
+            c3[j] = dv[j] * ex2_approx((float)(r3 - c));
+        }
+        float *q = tab + (slot * z.H + h0 + i) * kTab;
+        auto put = [&](int at, const float (&v)[4]) {
+            *reinterpret_cast<float4 *>(q + at + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+        };
+        put(kTabD, dv);
+        put(kTabL, lv);
+        put(kTabEc, ev);
+        put(kTabWf, wv);
+        if (blk < 1) put(col_at(1), c1);
+        if (blk < 2) put(col_at(2), c2);
+        if (blk < 3) put(col_at(3), c3);
     }
 }
 
-// Splits 8 bf16 times w into three planes: the sum of the planes is w x to 24 bits.
+// w x as three bf16 planes that add up to it exactly: each plane takes the top 8 bits
+// that are left (24 in all), by truncation.
 __device__ __forceinline__ void split3(uint4 x, float w, uint4 &hi, uint4 &mid, uint4 &lo)
 {
     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
@@ -73,231 +95,287 @@ __device__ __forceinline__ void split3(uint4 x, float w, uint4 &hi, uint4 &mid, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float v0 = w * umma::lo_f(in[i]), v1 = w * umma::hi_f(in[i]);
-        a[i] = umma::pack(v0, v1);
-        const float r0 = v0 - umma::lo_f(a[i]), r1 = v1 - umma::hi_f(a[i]);
-        b[i] = umma::pack(r0, r1);
-        c[i] = umma::pack(r0 - umma::lo_f(b[i]), r1 - umma::hi_f(b[i]));
+        const uint32_t u0 = __float_as_uint(v0), u1 = __float_as_uint(v1);
+        a[i] = __byte_perm(u0, u1, 0x7632);
+        const float r0 = v0 - __uint_as_float(u0 & 0xFFFF0000u), r1 = v1 - __uint_as_float(u1 & 0xFFFF0000u);
+        const uint32_t s0 = __float_as_uint(r0), s1 = __float_as_uint(r1);
+        b[i] = __byte_perm(s0, s1, 0x7632);
+        const float q0 = r0 - __uint_as_float(s0 & 0xFFFF0000u), q1 = r1 - __uint_as_float(s1 & 0xFFFF0000u);
+        c[i] = __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x7632);
     }
     hi = make_uint4(a[0], a[1], a[2], a[3]);
     mid = make_uint4(b[0], b[1], b[2], b[3]);
     lo = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
+constexpr int kConvWarps = 8, kStateWarps = 16;
+constexpr int kIssuer = kConvWarps + kStateWarps, kLoader = kIssuer + 1;
+constexpr int kStateThreads = (kLoader + 1) * 32;
+constexpr uint32_t kQuarter = 32 * 128;  // bytes of a 32-row panel
+
+// A stage: two x panels, the b tile, weights of the two panels' heads.
+template <int NPAD>
+constexpr uint32_t state_stage()
+{
+    return (2 + NPAD / 64) * umma::kPanel + 1024;
+}
 template <int NPAD>
 constexpr int state_smem()
 {
-    return 1024 + 6 * umma::kPanel + 2 * (NPAD / 64) * umma::kPanel + 2 * 2 * kC * 4 + 32;
+    return 1024 + 2 * 6 * kQuarter + 2 * state_stage<NPAD>();
 }
 
-// One CTA has two panels of one group and walks a segment's chunks. SEGMENT 0: a whole
-// sequence; 1: first pass of a split walk (from zero, only the end state); 2: second
-// pass (from the start states that head_join_kernel made).
-template <int NPAD, bool REV, int PLANES, int SEGMENT>
-__global__ void __launch_bounds__(256) head_state_kernel(StateArgs a)
+// One CTA has two panels of one group and walks a segment's chunks. The warps have
+// roles, so that loads, conversion, matrix instructions and state updates of
+// neighbouring chunks run at the same time (with all warps in step, each phase's
+// latency was exposed: 5500 clocks a chunk against 1536 of matrix instructions):
+//   loader     copies x, b and weights of the next chunk into one of two stages
+//   converters make w x as three planes, 32 tokens at a time, two buffers deep
+//   issuer     multiplies into one of two tensor-memory buffers
+//   state      keep the state in registers, write it before each chunk, add the product
+// `segment` 0: whole sequences; 1: first pass of a split walk (from zero, only the end
+// state); 2: second pass (from the start states that head_join_kernel made).
+template <int NPAD, bool REV, int PLANES, bool VEC>
+__global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, const __grid_constant__ CUtensorMap xmap,
+                                                                   const __grid_constant__ CUtensorMap bmap)
 {
-    constexpr int COLS = NPAD / 2;  // state columns of a thread
+    constexpr int COLS = NPAD / 4;  // state columns of a thread
     constexpr int BP = NPAD / 64;   // panels of a b tile
+    constexpr uint32_t STAGE = state_stage<NPAD>(), BUF = 6 * kQuarter;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bar;
+    // landed / used: a stage; made / eaten: a plane buffer; summed / taken: a product
+    __shared__ uint64_t landed[2], used[2], made[2], eaten[2], summed[2], taken[2];
     __shared__ uint32_t tmem_slot;
     const Dims &z = a.z;
-    const int tid = threadIdx.x, warp = tid / 32, wg = tid / 128, wt = tid % 128;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int64_t slot = blockIdx.x;
     const int pairs = (z.npan + 1) / 2, g = blockIdx.y / pairs, pair = blockIdx.y % pairs;
     const ChunkRef sg = find_chunk(z.cu, z.S, z.tok, a.span, slot);
-    if (sg.len == 0 && (sg.k != 0 || SEGMENT != 0)) return;
+    if (sg.len == 0 && (sg.k != 0 || a.segment != 0)) return;
     const int nchunk = (sg.len + kC - 1) / kC;
     int64_t lo, hi;
     seq_bounds(z.cu, z.S, z.tok, sg.seq, lo, hi);
     const int64_t first = lo / kC + sg.seq + (int64_t)sg.k * (a.span / kC);  // first chunk's slot
 
-    const uint32_t base = (saddr(raw) + 1023) & ~1023u;
-    const uint32_t sx = base, sb = base + 6 * umma::kPanel;
-    float *weights = reinterpret_cast<float *>(raw + (sb + 2 * BP * umma::kPanel - saddr(raw)));
-    float *decays = weights + 2 * 2 * kC;
-    if (tid == 0) mbar_init(&bar);
-    if (warp == 0) umma::alloc(&tmem_slot, NPAD == 128 ? 256 : 128);
+    const uint32_t planes = (saddr(raw) + 1023) & ~1023u, stages = planes + 2 * BUF;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init_n(&landed[i], 1);
+            mbar_init_n(&used[i], kConvWarps + 1);
+            mbar_init_n(&made[i], kConvWarps);
+            mbar_init_n(&eaten[i], 1);
+            mbar_init_n(&summed[i], 1);
+            mbar_init_n(&taken[i], kStateWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) umma::alloc(&tmem_slot, 2 * NPAD);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
     const uint32_t tm = tmem_slot;
-
-    // conversion side: this warpgroup's panel; state side: row wt (of both panels), COLS columns
-    const int xi = 2 * pair + wg, si = 2 * pair + wt / 64;
-    const bool has_x = xi < z.npan, has_s = si < z.npan;
-    const PanelRef xp = panel_of(z, g, min(xi, z.npan - 1)), sp = panel_of(z, g, min(si, z.npan - 1));
-    const int p = wt % 64, n0 = wg * COLS;
-    const bool row_in = has_s && p < sp.rows;
-    const bf16 *bsrc = a.b + (int64_t)g * z.N;
-    const bf16 *xsrc = a.x + (int64_t)xp.h * z.P + xp.p0;
-
-    float st[COLS];
-    {
-        const float *src = nullptr;
-        if (SEGMENT == 0 && a.init && row_in)
-            src = a.init + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
-        const float4 *sgp = nullptr;
-        if (SEGMENT == 2 && has_s)
-            sgp = reinterpret_cast<const float4 *>(
-                      a.seg + (slot * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
-#pragma unroll
-        for (int i = 0; i < COLS / 4; ++i) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (sgp) v = sgp[i * 64];
-            st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
-            if (src)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n0 + 4 * i + e < z.N) st[4 * i + e] = src[n0 + 4 * i + e];
-        }
-    }
-
-    uint4 xr[8];
-    double cn = 0.0, cq = 0.0;
-    float dn = 0.0f;
+    bool failed = false;
     auto chunk_at = [&](int kk) { return REV ? nchunk - 1 - kk : kk; };
-    auto load = [&](int kk) {
-        const int k = chunk_at(kk);
-        const int64_t t0 = sg.start + (int64_t)k * kC;
-        const int len = (int)min((int64_t)kC, sg.start + sg.len - t0);
-        load_tile<NPAD, 256>(sb + (kk & 1) * BP * umma::kPanel, bsrc + t0 * a.b_stride, a.b_stride, len,
-                             z.N, a.b_vec, tid);
-        umma::cp_commit();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 16 * i + wt / 8, c = wt % 8;
-            const int n = has_x && r < len ? min(8, xp.rows - 8 * c) : 0;
-            const bf16 *q = xsrc + (t0 + r) * a.x_stride + 8 * c;
-            xr[i] = n <= 0 ? make_uint4(0, 0, 0, 0) : a.x_vec ? ldg16(q) : read8(q, n);
-        }
-        const int64_t at = ((first + k) * z.H + xp.h) * kC;
-        cn = a.c[at + wt];
-        cq = a.c[at + kC - 1];
-        dn = a.d[at + wt];
-    };
-    auto set_weights = [&](int kk) {
-        weights[(kk & 1) * 256 + tid] =
-            REV ? ex2_approx((float)cn) : dn * ex2_approx((float)(cq - cn));
-        // four deep: a slow warp may still be at chunk kk - 2
-        if (wt == 0) decays[(kk & 3) * 2 + wg] = ex2_approx((float)cq);
-    };
-    auto step = [&](int kk) {  // st = decay st + product of chunk kk
-        const float e = decays[(kk & 3) * 2 + wt / 64];
-#pragma unroll
-        for (int j = 0; j < COLS / 32; ++j) {
-            uint32_t v[32];
-            umma::ld32(umma::lanes(tm + (kk & 1) * NPAD + n0 + 32 * j, warp), v);
-            umma::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                st[32 * j + i] = fmaf(e, st[32 * j + i], __uint_as_float(v[i]));
-        }
-    };
-    auto mark = [&](int kk) {
-        if (SEGMENT == 1 || !has_s) return;
-        bf16 *m = a.marks + ((first + chunk_at(kk)) * z.G * z.npan + g * z.npan + si) * PLANES * kMark<NPAD>;
-        uint4 *q = reinterpret_cast<uint4 *>(m) + (n0 / 8) * 64 + p;
-#pragma unroll
-        for (int j = 0; j < COLS / 8; ++j) {
-            uint32_t w[PLANES][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v0 = st[8 * j + 2 * i], v1 = st[8 * j + 2 * i + 1];
-#pragma unroll
-                for (int s = 0; s < PLANES; ++s) {
-                    w[s][i] = umma::pack(v0, v1);
-                    v0 -= umma::lo_f(w[s][i]);
-                    v1 -= umma::hi_f(w[s][i]);
+    auto len_of = [&](int k) { return min(kC, sg.len - k * kC); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, failed, &g_status); };
+
+    if (warp == kLoader) {
+        const int np = min(2, z.npan - 2 * pair);  // panels there are
+        const PanelRef q0 = panel_of(z, g, 2 * pair), q1 = panel_of(z, g, 2 * pair + np - 1);
+        for (int kk = 0; kk < nchunk; ++kk) {
+            const int k = chunk_at(kk);
+            const int64_t t0 = sg.start + (int64_t)k * kC;
+            const uint32_t sx = stages + (kk & 1) * STAGE, sb = sx + 2 * umma::kPanel, sw = sb + BP * umma::kPanel;
+            uint64_t *bar = &landed[kk & 1];
+            if (kk >= 2) wait(&used[kk & 1], (kk >> 1) - 1);
+            if (!VEC) {
+                const int len = len_of(k);
+                load_tile_warp<64>(sx, a.x + t0 * a.x_stride + (int64_t)q0.h * z.P + q0.p0, a.x_stride, len, q0.rows, lane);
+                if (np > 1)
+                    load_tile_warp<64>(sx + umma::kPanel, a.x + t0 * a.x_stride + (int64_t)q1.h * z.P + q1.p0,
+                                       a.x_stride, len, q1.rows, lane);
+                load_tile_warp<NPAD>(sb, a.b + t0 * a.b_stride + (int64_t)g * z.N, a.b_stride, len, z.N, lane);
+                fence_proxy_async();
+            }
+            __syncwarp();
+            if (umma::elect()) {
+                const float *w0 = a.tab + ((first + k) * z.H + q0.h) * kTab + (REV ? kTabEc : kTabWf);
+                const float *w1 = a.tab + ((first + k) * z.H + q1.h) * kTab + (REV ? kTabEc : kTabWf);
+                mbar_expect_tx(bar, 1024 + (VEC ? (np + BP) * umma::kPanel : 0));
+                umma::bulk_load(sw, w0, 512, bar);
+                umma::bulk_load(sw + 512, w1, 512, bar);
+                if (VEC) {
+                    umma::tma_3d(sx, &xmap, bar, q0.p0, q0.h, (int)t0);
+                    if (np > 1) umma::tma_3d(sx + umma::kPanel, &xmap, bar, q1.p0, q1.h, (int)t0);
+                    for (int i = 0; i < BP; ++i) umma::tma_3d(sb + i * umma::kPanel, &bmap, bar, 64 * i, g, (int)t0);
                 }
             }
-#pragma unroll
-            for (int s = 0; s < PLANES; ++s)
-                q[(s * (NPAD / 8) + j) * 64] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+            __syncwarp();
         }
-    };
-
-    bool failed = false;
-    if (nchunk > 0) {
-        load(0);
-        set_weights(0);
-    }
-    __syncthreads();
-    for (int kk = 0; kk < nchunk; ++kk) {
-        if (kk > 0) mbar_wait(&bar, (kk - 1) & 1, failed, &g_status, 1);
-        umma::fence_after();
+    } else if (warp == kIssuer) {
+        if (umma::elect()) {
+            for (int kk = 0; kk < nchunk; ++kk) {
+                const uint32_t sb = stages + (kk & 1) * STAGE + 2 * umma::kPanel, d = tm + (kk & 1) * NPAD;
+                wait(&landed[kk & 1], kk >> 1);
+                if (kk >= 2) wait(&taken[kk & 1], (kk >> 1) - 1);
+                for (int q = 0; q < 4; ++q) {
+                    wait(&made[q & 1], 2 * kk + (q >> 1));
+                    umma::fence_after();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 16 * i + wt / 8, c = wt % 8;
-            uint4 hi4, mid4, lo4;
-            split3(xr[i], weights[(kk & 1) * 256 + wg * 128 + r], hi4, mid4, lo4);
-            const uint32_t at = sx + wg * umma::kPanel + umma::piece(r, c);
-            sts16(at, hi4);
-            sts16(at + 2 * umma::kPanel, mid4);
-            sts16(at + 4 * umma::kPanel, lo4);
-        }
-        if (kk + 1 < nchunk) {
-            load(kk + 1);
-            umma::cp_wait<1>();
-        } else {
-            umma::cp_wait<0>();
-        }
-        fence_proxy_async();
-        umma::fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            umma::fence_after();
-            const uint32_t bt = sb + (kk & 1) * BP * umma::kPanel;
-            for (int s = 0; s < 3; ++s)
+                    for (int s = 0; s < 3; ++s)
 #pragma unroll
-                for (int k16 = 0; k16 < 8; ++k16)
-                    umma::mma(tm + (kk & 1) * NPAD,
-                              umma::desc_mn(sx + 2 * s * umma::kPanel, k16, umma::kPanel),
-                              umma::desc_mn(bt, k16, umma::kPanel), umma::idesc(NPAD, true, true),
-                              s + k16 > 0);
-            umma::commit(&bar);
+                        for (int k = 0; k < 2; ++k)
+                            umma::mma(d, umma::desc_mn(planes + (q & 1) * BUF + s * 2 * kQuarter, k, kQuarter),
+                                      umma::desc_mn(sb, 2 * q + k, umma::kPanel), umma::idesc(NPAD, true, true),
+                                      q + s + k > 0);
+                    umma::commit(&eaten[q & 1]);
+                }
+                umma::commit(&summed[kk & 1]);
+                umma::commit(&used[kk & 1]);
+            }
         }
         __syncwarp();
-        if (kk > 0) step(kk - 1);
-        mark(kk);
-        if (kk + 1 < nchunk) set_weights(kk + 1);
-        umma::fence_before();
-        __syncthreads();
-    }
-    if (nchunk > 0) {
-        mbar_wait(&bar, (nchunk - 1) & 1, failed, &g_status, 1);
-        umma::fence_after();
-        step(nchunk - 1);
-    }
-    if (SEGMENT == 0 && a.final_ && row_in) {
-        float *dst = a.final_ + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
-        const bool v4 = z.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.final_) % 16 == 0;
+    } else if (warp < kConvWarps) {
+        // panel cp; rows r0 and r0 + 16 of every 32, piece c8
+        const int cp = tid / 128, r0 = tid % 128 / 8, c8 = tid % 8;
+        const bool has_x = 2 * pair + cp < z.npan;
+        for (int kk = 0; kk < nchunk; ++kk) {
+            const int len = len_of(chunk_at(kk));
+            const uint32_t sx = stages + (kk & 1) * STAGE, sb = sx + 2 * umma::kPanel;
+            const float *w = reinterpret_cast<const float *>(raw + (sb + BP * umma::kPanel + cp * 512 - saddr(raw)));
+            wait(&landed[kk & 1], kk >> 1);
+            if (VEC && len < kC) zero_tail(sb, BP, len, tid, kConvWarps * 32);
+            const uint32_t from = sx + cp * umma::kPanel + umma::piece(r0, c8);
+            const uint32_t to = planes + cp * kQuarter + umma::piece(r0, c8);
 #pragma unroll
-        for (int i = 0; i < COLS / 4; ++i) {
-            const int n = n0 + 4 * i;
-            if (v4 && n < z.N)
-                *reinterpret_cast<float4 *>(dst + n) =
-                    make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
-            else
+            for (int q = 0; q < 4; ++q) {
+                uint4 v[2][3];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < z.N) dst[n + e] = st[4 * i + e];
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 32 * q + 16 * i;
+                    const uint4 x = has_x && r + r0 < len ? lds16(from + r * 128) : make_uint4(0, 0, 0, 0);
+                    split3(x, w[r + r0], v[i][0], v[i][1], v[i][2]);
+                }
+                if (kk > 0 || q >= 2) wait(&eaten[q & 1], 2 * kk + (q >> 1) - 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int s = 0; s < 3; ++s)
+                        sts16(to + (q & 1) * BUF + s * 2 * kQuarter + 16 * i * 128, v[i][s]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&made[q & 1]);
+            }
+            if (lane == 0) mbar_arrive(&used[kk & 1]);
         }
-    }
-    if (SEGMENT == 1 && has_s) {
-        float4 *q = reinterpret_cast<float4 *>(
-                        a.seg + (slot * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
+    } else {
+        // row sr of the two panels, columns n0 ..
+        const int sw = warp - kConvWarps, sr = (sw & 3) * 32 + lane, n0 = (sw / 4) * COLS;
+        const int si = 2 * pair + sr / 64, p = sr % 64;
+        const bool has_s = si < z.npan;
+        const PanelRef sp = panel_of(z, g, min(si, z.npan - 1));
+        const bool row_in = has_s && p < sp.rows;
+        const int64_t dir = REV ? -1 : 1, c0 = first + chunk_at(0);
+        const float *dec = a.tab + (c0 * z.H + sp.h) * kTab + kTabEc + kC - 1;
+        const int64_t dec_step = dir * z.H * kTab;
+
+        float st[COLS];
+        {
+            const float *src = nullptr;
+            if (a.segment == 0 && a.init && row_in)
+                src = a.init + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
+            const float4 *sgp = nullptr;
+            if (a.segment == 2 && has_s)
+                sgp = reinterpret_cast<const float4 *>(
+                          a.seg + (slot * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
 #pragma unroll
-        for (int i = 0; i < COLS / 4; ++i)
-            q[i * 64] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
-        if (wg == 0 && p == 0) {
-            double t = 0.0;
-            for (int k = 0; k < nchunk; ++k) t += a.c[((first + k) * z.H + sp.h) * kC + kC - 1];
-            a.segdec[slot * z.H + sp.h] = t;
+            for (int i = 0; i < COLS / 4; ++i) {
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (sgp) v = sgp[i * 64];
+                st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
+                if (src)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n0 + 4 * i + e < z.N) st[4 * i + e] = src[n0 + 4 * i + e];
+            }
+        }
+        uint4 *mk = reinterpret_cast<uint4 *>(
+                        a.marks + (c0 * z.G * z.npan + g * z.npan + si) * PLANES * kMark<NPAD>) + (n0 / 8) * 64 + p;
+        const int64_t mk_step = dir * z.G * z.npan * PLANES * kMark<NPAD> / 8;
+        const bool marking = a.segment != 1 && has_s;
+        float e = nchunk > 0 ? *dec : 1.0f;
+        for (int kk = 0; kk < nchunk; ++kk) {
+            if (marking) {
+#pragma unroll
+                for (int j = 0; j < COLS / 8; ++j) {
+                    uint32_t w[PLANES][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v0 = st[8 * j + 2 * i], v1 = st[8 * j + 2 * i + 1];
+#pragma unroll
+                        for (int s = 0; s < PLANES; ++s) {
+                            w[s][i] = umma::pack(v0, v1);
+                            v0 -= umma::lo_f(w[s][i]);
+                            v1 -= umma::hi_f(w[s][i]);
+                        }
+                    }
+#pragma unroll
+                    for (int s = 0; s < PLANES; ++s)
+                        mk[(s * (NPAD / 8) + j) * 64] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+                }
+                mk += mk_step;
+            }
+            const float now = e;
+            if (kk + 1 < nchunk) {
+                dec += dec_step;
+                e = *dec;
+            }
+            wait(&summed[kk & 1], kk >> 1);
+            umma::fence_after();
+#pragma unroll
+            for (int j = 0; j < COLS / 16; ++j) {
+                uint32_t v[16];
+                umma::ld16(umma::lanes(tm + (kk & 1) * NPAD + n0 + 16 * j, warp), v);
+                umma::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    st[16 * j + i] = fmaf(now, st[16 * j + i], __uint_as_float(v[i]));
+            }
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&taken[kk & 1]);
+        }
+        if (a.segment == 0 && a.final_ && row_in) {
+            float *dst = a.final_ + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
+            const bool v4 = z.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.final_) % 16 == 0;
+#pragma unroll
+            for (int i = 0; i < COLS / 4; ++i) {
+                const int n = n0 + 4 * i;
+                if (v4 && n < z.N)
+                    *reinterpret_cast<float4 *>(dst + n) =
+                        make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+                else
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (n + x < z.N) dst[n + x] = st[4 * i + x];
+            }
+        }
+        if (a.segment == 1 && has_s) {
+            float4 *q = reinterpret_cast<float4 *>(
+                            a.seg + (slot * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
+#pragma unroll
+            for (int i = 0; i < COLS / 4; ++i)
+                q[i * 64] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+            if (n0 == 0 && p == 0) {
+                float t = 1.0f;
+                for (int k = 0; k < nchunk; ++k) t *= a.tab[((first + k) * z.H + sp.h) * kTab + kTabEc + kC - 1];
+                a.segdec[slot * z.H + sp.h] = t;
+            }
         }
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == 0) umma::dealloc(tm, NPAD == 128 ? 256 : 128);
+    if (warp == 0) umma::dealloc(tm, 2 * NPAD);
 }
 
 // One block per (sequence, panel): turns the segments' end states from zero into their
@@ -325,7 +403,7 @@ __global__ void __launch_bounds__(256) head_join_kernel(StateArgs a)
             const int64_t slot = base + (REV ? nseg - 1 - k : k);
             float4 *q = reinterpret_cast<float4 *>(a.seg + (slot * z.G * z.npan + g * z.npan + pi) * 64 * NPAD) + x;
             const float4 end = *q;
-            const float dec = ex2_approx((float)a.segdec[slot * z.H + pr.h]);
+            const float dec = a.segdec[slot * z.H + pr.h];
             *q = v;
             v.x = fmaf(dec, v.x, end.x);
             v.y = fmaf(dec, v.y, end.y);
@@ -338,29 +416,39 @@ __global__ void __launch_bounds__(256) head_join_kernel(StateArgs a)
     }
 }
 
-template <int NPAD, bool REV, int PLANES, int SEGMENT>
+template <int NPAD, bool REV, int PLANES, bool VEC>
 cudaError_t launch_walk(const StateArgs &a, cudaStream_t st, int *launches)
 {
     constexpr int bytes = state_smem<NPAD>();
-    if (cudaError_t e = cudaFuncSetAttribute(head_state_kernel<NPAD, REV, PLANES, SEGMENT>,
+    if (cudaError_t e = cudaFuncSetAttribute(head_state_kernel<NPAD, REV, PLANES, VEC>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)head_slots(a.z.tok, a.z.S, a.span), (unsigned)(a.z.G * ((a.z.npan + 1) / 2)));
-    head_state_kernel<NPAD, REV, PLANES, SEGMENT><<<grid, 256, bytes, st>>>(a);
+    CUtensorMap xmap{}, bmap{};
+    if (VEC && a.z.tok > 0 &&
+        (!umma::encode_3d(&xmap, a.x, a.z.tok, a.z.H, a.z.P, a.x_stride) ||
+         !umma::encode_3d(&bmap, a.b, a.z.tok, a.z.G, a.z.N, a.b_stride)))
+        return cudaErrorInvalidValue;
+    head_state_kernel<NPAD, REV, PLANES, VEC><<<grid, kStateThreads, bytes, st>>>(a, xmap, bmap);
     ++*launches;
     return cudaGetLastError();
 }
 
 template <int NPAD, bool REV, int PLANES>
-cudaError_t states(const StateArgs &a, bool split, cudaStream_t st, int *launches)
+cudaError_t states(StateArgs a, bool split, bool vec, cudaStream_t st, int *launches)
 {
-    if (!split) return launch_walk<NPAD, REV, PLANES, 0>(a, st, launches);
-    if (cudaError_t e = launch_walk<NPAD, REV, PLANES, 1>(a, st, launches); e != cudaSuccess) return e;
+    auto walk = [&](int segment) {
+        a.segment = segment;
+        return vec ? launch_walk<NPAD, REV, PLANES, true>(a, st, launches)
+                   : launch_walk<NPAD, REV, PLANES, false>(a, st, launches);
+    };
+    if (!split) return walk(0);
+    if (cudaError_t e = walk(1); e != cudaSuccess) return e;
     head_join_kernel<NPAD, REV><<<dim3((unsigned)a.z.S, (unsigned)(a.z.G * a.z.npan)), 256, 0, st>>>(a);
     ++*launches;
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    return launch_walk<NPAD, REV, PLANES, 2>(a, st, launches);
+    return walk(2);
 }
 
 }  // namespace
@@ -394,27 +482,41 @@ int64_t segment_span(const Dims &z, bool *split)
     return seg * kC;
 }
 
-cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, double *c, float *d,
-                          cudaStream_t stream, int *launches)
+cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, cudaStream_t stream,
+                          int *launches)
 {
     const dim3 grid((unsigned)head_slots(z.tok, z.S, kC), (unsigned)((z.H + 31) / 32));
     head_table_kernel<<<grid, 256, 0, stream>>>(z, static_cast<const bf16 *>(a.delta), a.delta_stride,
-                                                a.A, a.dt_bias, a.delta_softplus, c, d);
+                                                a.A, a.dt_bias, a.delta_softplus, tab);
     ++*launches;
     return cudaGetLastError();
 }
 
-cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, cudaStream_t st,
-                          int *launches)
+cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, bool vec,
+                          cudaStream_t st, int *launches)
 {
     const bool wide = a.z.N > 64;
     if (planes == 1)
-        return wide ? states<128, false, 1>(a, split, st, launches)
-                    : states<64, false, 1>(a, split, st, launches);
-    if (rev) return wide ? states<128, true, 2>(a, split, st, launches)
-                         : states<64, true, 2>(a, split, st, launches);
-    return wide ? states<128, false, 2>(a, split, st, launches)
-                : states<64, false, 2>(a, split, st, launches);
+        return wide ? states<128, false, 1>(a, split, vec, st, launches)
+                    : states<64, false, 1>(a, split, vec, st, launches);
+    if (rev) return wide ? states<128, true, 2>(a, split, vec, st, launches)
+                         : states<64, true, 2>(a, split, vec, st, launches);
+    return wide ? states<128, false, 2>(a, split, vec, st, launches)
+                : states<64, false, 2>(a, split, vec, st, launches);
+}
+
+Layout layout_of(const Dims &z, int planes, int64_t span, bool split)
+{
+    const int64_t slots = head_slots(z.tok, z.S, kC), segs = split ? head_slots(z.tok, z.S, span) : 0;
+    const int npad = z.N > 64 ? 128 : 64;
+    const size_t panel = (size_t)z.G * z.npan * 64 * npad;
+    Layout l;
+    l.tab = 0;
+    l.seg = l.tab + up256((size_t)slots * z.H * kTab * 4);
+    l.segdec = l.seg + up256((size_t)segs * panel * 4);
+    l.marks = l.segdec + up256((size_t)segs * z.H * 4);
+    l.total = l.marks + up256((size_t)slots * panel * 2 * planes);
+    return l;
 }
 
 }  // namespace hm

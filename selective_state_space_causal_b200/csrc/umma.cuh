@@ -38,11 +38,39 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t panel, int k16, uint32_t ne
     return desc(panel + k16 * 2048, next, 1024);
 }
 
+// Tiles without swizzle, as the state marks are kept: pieces of 8 bf16, [piece][row][8],
+// `rows` rows. K-major when the pieces run along K, MN-major when the rows do.
+__device__ __forceinline__ uint64_t desc_plain(uint32_t addr, uint32_t lead, uint32_t stride)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lead >> 4) << 16) |
+           ((uint64_t)(stride >> 4) << 32) | ((uint64_t)1 << 46);
+}
+__device__ __forceinline__ uint64_t plain_k(uint32_t tile, int k16, int rows)
+{
+    return desc_plain(tile + k16 * 32 * rows, 16 * rows, 128);
+}
+__device__ __forceinline__ uint64_t plain_mn(uint32_t tile, int k16, int rows)
+{
+    return desc_plain(tile + k16 * 256, 128, 16 * rows);
+}
+
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 128.
 __device__ __forceinline__ constexpr uint32_t idesc(int N, bool a_mn, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// True in one lane of a converged warp. The matrix instructions of a warp are issued
+// under it: the compiler then knows that one thread runs them and keeps descriptors in
+// uniform registers, which a test of the thread index does not tell it (100 clocks an
+// instruction instead of the 32 to 64 that the tensor core takes).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) :: "memory");
+    return r != 0;
 }
 
 // D (+)= A B, operands in shared memory. One thread.
@@ -87,6 +115,24 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// mbar_wait for barriers that matrix instructions complete: these waits are short and
+// on the critical path, so they poll with the hardware's own suspend time. At most 2^22
+// tries, then bit 1 of *status is set and this thread waits no more.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &failed, int *status)
+{
+    if (failed) return;
+    for (unsigned i = 0; i < 1u << 22; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done) : "r"(saddr(bar)), "r"(parity) : "memory");
+        if (done) return;
+    }
+    failed = true;
+    atomicOr(status, 1);
+}
+
 // Address of this warp's lanes: a warp reaches lanes 32 (warp % 4) .. + 31.
 __device__ __forceinline__ uint32_t lanes(uint32_t base, int warp) { return base + ((uint32_t)(warp & 3) << 21); }
 
@@ -102,6 +148,23 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t (&v)[32])
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
+}
+
+__device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
@@ -134,6 +197,43 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait()
 {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+// 3-D tile load / store; a store's completion is tracked by bulk groups.
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 :: "l"(map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        :: "r"(dst), "l"(src), "r"(bytes), "r"(saddr(bar)) : "memory");
+}
+
+// (tokens, groups, width) bf16 with a token stride, in boxes of 128 tokens x 64 columns
+// of one group, 128-byte swizzle; columns beyond `width` and tokens beyond the last read
+// as zeros and are not stored. Base 16-byte aligned, stride and width multiples of 8.
+inline bool encode_3d(CUtensorMap *map, const void *base, int64_t tokens, int64_t groups, int64_t width,
+                      int64_t stride)
+{
+    auto fn = tensor_map_encoder();
+    if (!fn || tokens < 1) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)groups, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace umma
