@@ -86,32 +86,27 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
     }
 }
 
-// w x as three bf16 planes that add up to it exactly: each plane takes the top 8 bits
-// that are left (24 in all), by truncation.
-__device__ __forceinline__ void split3(uint4 x, float w, uint4 &hi, uint4 &mid, uint4 &lo)
+// Two neighbouring tokens' w x as three pairs of bf16 that add up to it exactly: each
+// takes the top 8 bits that are left (24 in all), by truncation.
+__device__ __forceinline__ void split3(uint32_t x, f32x2 w, uint32_t &hi, uint32_t &mid, uint32_t &lo)
 {
-    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-    uint32_t a[4], b[4], c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float v0 = w * umma::lo_f(in[i]), v1 = w * umma::hi_f(in[i]);
-        const uint32_t u0 = __float_as_uint(v0), u1 = __float_as_uint(v1);
-        a[i] = __byte_perm(u0, u1, 0x7632);
-        const float r0 = v0 - __uint_as_float(u0 & 0xFFFF0000u), r1 = v1 - __uint_as_float(u1 & 0xFFFF0000u);
-        const uint32_t s0 = __float_as_uint(r0), s1 = __float_as_uint(r1);
-        b[i] = __byte_perm(s0, s1, 0x7632);
-        const float q0 = r0 - __uint_as_float(s0 & 0xFFFF0000u), q1 = r1 - __uint_as_float(s1 & 0xFFFF0000u);
-        c[i] = __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x7632);
-    }
-    hi = make_uint4(a[0], a[1], a[2], a[3]);
-    mid = make_uint4(b[0], b[1], b[2], b[3]);
-    lo = make_uint4(c[0], c[1], c[2], c[3]);
+    const f32x2 minus = pk2(-1.0f, -1.0f);
+    f32x2 v = mul2(pk2(umma::lo_f(x), umma::hi_f(x)), w);
+    float v0, v1;
+    upk2(v, v0, v1);
+    hi = __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632);
+    v = fma2(pk2(umma::hi_f(__float_as_uint(v0)), umma::hi_f(__float_as_uint(v1))), minus, v);
+    upk2(v, v0, v1);
+    mid = __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632);
+    v = fma2(pk2(umma::hi_f(__float_as_uint(v0)), umma::hi_f(__float_as_uint(v1))), minus, v);
+    upk2(v, v0, v1);
+    lo = __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632);
 }
 
-constexpr int kConvWarps = 8, kStateWarps = 16;
+constexpr int kGroups = 3, kConvWarps = 4 * kGroups, kStateWarps = 16;
 constexpr int kIssuer = kConvWarps + kStateWarps, kLoader = kIssuer + 1;
 constexpr int kStateThreads = (kLoader + 1) * 32;
-constexpr uint32_t kQuarter = 32 * 128;  // bytes of a 32-row panel
+constexpr int kStages = 3;
 
 // A stage: two x panels, the b tile, weights of the two panels' heads.
 template <int NPAD>
@@ -122,15 +117,17 @@ constexpr uint32_t state_stage()
 template <int NPAD>
 constexpr int state_smem()
 {
-    return 1024 + 2 * 6 * kQuarter + 2 * state_stage<NPAD>();
+    return 1024 + kStages * state_stage<NPAD>();
 }
 
 // One CTA has two panels of one group and walks a segment's chunks. The warps have
 // roles, so that loads, conversion, matrix instructions and state updates of
 // neighbouring chunks run at the same time (with all warps in step, each phase's
 // latency was exposed: 5500 clocks a chunk against 1536 of matrix instructions):
-//   loader     copies x, b and weights of the next chunk into one of two stages
-//   converters make w x as three planes, 32 tokens at a time, two buffers deep
+//   loader     copies x, b and weights of the next chunks into one of three stages
+//   converters make w x as three planes in tensor memory, transposed on the way, 32
+//              tokens at a time, three groups of four warps in turn. (Planes in shared
+//              memory cost it 384 KB of traffic a chunk, 3000 clocks, against 192 KB.)
 //   issuer     multiplies into one of two tensor-memory buffers
 //   state      keep the state in registers, write it before each chunk, add the product
 // `segment` 0: whole sequences; 1: first pass of a split walk (from zero, only the end
@@ -141,10 +138,10 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
 {
     constexpr int COLS = NPAD / 4;  // state columns of a thread
     constexpr int BP = NPAD / 64;   // panels of a b tile
-    constexpr uint32_t STAGE = state_stage<NPAD>(), BUF = 6 * kQuarter;
+    constexpr uint32_t STAGE = state_stage<NPAD>();
     extern __shared__ uint8_t raw[];
-    // landed / used: a stage; made / eaten: a plane buffer; summed / taken: a product
-    __shared__ uint64_t landed[2], used[2], made[2], eaten[2], summed[2], taken[2];
+    // landed / used: a stage; made / eaten: 32 tokens' planes; summed / taken: a product
+    __shared__ uint64_t landed[kStages], used[kStages], made[4], eaten[4], summed[2], taken[2];
     __shared__ uint32_t tmem_slot;
     const Dims &z = a.z;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -157,23 +154,27 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     seq_bounds(z.cu, z.S, z.tok, sg.seq, lo, hi);
     const int64_t first = lo / kC + sg.seq + (int64_t)sg.k * (a.span / kC);  // first chunk's slot
 
-    const uint32_t planes = (saddr(raw) + 1023) & ~1023u, stages = planes + 2 * BUF;
+    const uint32_t stages = (saddr(raw) + 1023) & ~1023u;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init_n(&landed[i], 1);
-            mbar_init_n(&used[i], kConvWarps + 1);
-            mbar_init_n(&made[i], kConvWarps);
+            mbar_init_n(&used[i], 4 * 4 + 1);  // four warps for each 32 tokens, and the products
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init_n(&made[i], 4);
             mbar_init_n(&eaten[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init_n(&summed[i], 1);
             mbar_init_n(&taken[i], kStateWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) umma::alloc(&tmem_slot, 2 * NPAD);
+    if (warp == 0) umma::alloc(&tmem_slot, 512);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    const uint32_t tm = tmem_slot;
+    const uint32_t tm = tmem_slot, planes = tm + 256;  // two products, then 4 x 3 planes of 16 columns
     bool failed = false;
     auto chunk_at = [&](int kk) { return REV ? nchunk - 1 - kk : kk; };
     auto len_of = [&](int k) { return min(kC, sg.len - k * kC); };
@@ -183,11 +184,11 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
         const int np = min(2, z.npan - 2 * pair);  // panels there are
         const PanelRef q0 = panel_of(z, g, 2 * pair), q1 = panel_of(z, g, 2 * pair + np - 1);
         for (int kk = 0; kk < nchunk; ++kk) {
-            const int k = chunk_at(kk);
+            const int k = chunk_at(kk), sg_i = kk % kStages;
             const int64_t t0 = sg.start + (int64_t)k * kC;
-            const uint32_t sx = stages + (kk & 1) * STAGE, sb = sx + 2 * umma::kPanel, sw = sb + BP * umma::kPanel;
-            uint64_t *bar = &landed[kk & 1];
-            if (kk >= 2) wait(&used[kk & 1], (kk >> 1) - 1);
+            const uint32_t sx = stages + sg_i * STAGE, sb = sx + 2 * umma::kPanel, sw = sb + BP * umma::kPanel;
+            uint64_t *bar = &landed[sg_i];
+            if (kk >= kStages) wait(&used[sg_i], kk / kStages - 1);
             if (!VEC) {
                 const int len = len_of(k);
                 load_tile_warp<64>(sx, a.x + t0 * a.x_stride + (int64_t)q0.h * z.P + q0.p0, a.x_stride, len, q0.rows, lane);
@@ -215,58 +216,85 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     } else if (warp == kIssuer) {
         if (umma::elect()) {
             for (int kk = 0; kk < nchunk; ++kk) {
-                const uint32_t sb = stages + (kk & 1) * STAGE + 2 * umma::kPanel, d = tm + (kk & 1) * NPAD;
-                wait(&landed[kk & 1], kk >> 1);
+                const uint32_t sb = stages + kk % kStages * STAGE + 2 * umma::kPanel, d = tm + (kk & 1) * NPAD;
+                wait(&landed[kk % kStages], kk / kStages);
                 if (kk >= 2) wait(&taken[kk & 1], (kk >> 1) - 1);
                 for (int q = 0; q < 4; ++q) {
-                    wait(&made[q & 1], 2 * kk + (q >> 1));
+                    wait(&made[q], kk);
                     umma::fence_after();
 #pragma unroll
                     for (int s = 0; s < 3; ++s)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            umma::mma(d, umma::desc_mn(planes + (q & 1) * BUF + s * 2 * kQuarter, k, kQuarter),
-                                      umma::desc_mn(sb, 2 * q + k, umma::kPanel), umma::idesc(NPAD, true, true),
-                                      q + s + k > 0);
-                    umma::commit(&eaten[q & 1]);
+                            umma::mma_ta(d, planes + (3 * q + s) * 16 + 8 * k,
+                                         umma::desc_mn(sb, 2 * q + k, umma::kPanel), umma::idesc(NPAD, false, true),
+                                         q + s + k > 0);
+                    umma::commit(&eaten[q]);
                 }
                 umma::commit(&summed[kk & 1]);
-                umma::commit(&used[kk & 1]);
+                umma::commit(&used[kk % kStages]);
             }
         }
         __syncwarp();
     } else if (warp < kConvWarps) {
-        // panel cp; rows r0 and r0 + 16 of every 32, piece c8
-        const int cp = tid / 128, r0 = tid % 128 / 8, c8 = tid % 8;
+        // 32 tokens at a time; this warp has state rows 32 (warp % 4) .. of the two panels
+        const int grp = warp / 4, w4 = warp % 4, cp = w4 / 2;
         const bool has_x = 2 * pair + cp < z.npan;
-        for (int kk = 0; kk < nchunk; ++kk) {
-            const int len = len_of(chunk_at(kk));
-            const uint32_t sx = stages + (kk & 1) * STAGE, sb = sx + 2 * umma::kPanel;
-            const float *w = reinterpret_cast<const float *>(raw + (sb + BP * umma::kPanel + cp * 512 - saddr(raw)));
-            wait(&landed[kk & 1], kk >> 1);
-            if (VEC && len < kC) zero_tail(sb, BP, len, tid, kConvWarps * 32);
-            const uint32_t from = sx + cp * umma::kPanel + umma::piece(r0, c8);
-            const uint32_t to = planes + cp * kQuarter + umma::piece(r0, c8);
+        const uint32_t rows = (uint32_t)w4 << 21;
+        // the tiles of ldsm_t: tokens 0-7, rows 0-7; the same tokens, rows 8-15; tokens 8-15
+        const int tt = lane % 8 + (lane / 16) * 8, pc = (w4 & 1) * 4 + (lane / 8) % 2;
+        for (int j = grp; j < 4 * nchunk; j += kGroups) {
+            const int kk = j / 4, q = j % 4, st = kk % kStages;
+            const int len = len_of(chunk_at(kk)) - 32 * q;  // tokens left from here
+            const uint32_t sx = stages + st * STAGE, sb = sx + 2 * umma::kPanel;
+            const float2 *w = reinterpret_cast<const float2 *>(
+                raw + (sb + BP * umma::kPanel + cp * 512 + q * 128 - saddr(raw))) + lane % 4;
+            wait(&landed[st], kk / kStages);
+            if (kk > 0) wait(&eaten[q], kk - 1);
+            umma::fence_after();
+            f32x2 wt[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint4 v[2][3];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 32 * q + 16 * i;
-                    const uint4 x = has_x && r + r0 < len ? lds16(from + r * 128) : make_uint4(0, 0, 0, 0);
-                    split3(x, w[r + r0], v[i][0], v[i][1], v[i][2]);
-                }
-                if (kk > 0 || q >= 2) wait(&eaten[q & 1], 2 * kk + (q >> 1) - 1);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int s = 0; s < 3; ++s)
-                        sts16(to + (q & 1) * BUF + s * 2 * kQuarter + 16 * i * 128, v[i][s]);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&made[q & 1]);
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = w[4 * i];  // tokens 8 i + 2 (lane % 4) and + 1
+                wt[i] = pk2(v.x, v.y);
             }
-            if (lane == 0) mbar_arrive(&used[kk & 1]);
+            if (len < 32) {  // tokens behind the sequence: b's rows become zeros (x's do below)
+                for (int i = tid % 128; i < 32 * BP * 8; i += 128) {
+                    const int r = i / (BP * 8), c = i % (BP * 8);
+                    if (r >= len)
+                        sts16(sb + (c / 8) * umma::kPanel + umma::piece(32 * q + r, c % 8), make_uint4(0, 0, 0, 0));
+                }
+                fence_proxy_async();
+            }
+#pragma unroll
+            for (int ph = 0; ph < 2; ++ph) {  // 16 state rows
+                uint32_t x[8], v[3][8];
+#pragma unroll
+                for (int th = 0; th < 2; ++th)  // 16 tokens
+                    umma::ldsm_t(sx + cp * umma::kPanel + umma::piece(32 * q + 16 * th + tt, pc + 2 * ph),
+                                 x[4 * th], x[4 * th + 1], x[4 * th + 2], x[4 * th + 3]);
+                if (len < 32 || !has_x) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = 8 * (i / 2) + 2 * (lane % 4);
+                        const uint32_t keep = (t < len ? 0xFFFFu : 0u) | (t + 1 < len ? 0xFFFF0000u : 0u);
+                        x[i] &= has_x ? keep : 0u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split3(x[i], wt[i / 2], v[0][i], v[1][i], v[2][i]);
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                    umma::st_tiles(planes + rows + ((uint32_t)ph << 20) + (3 * q + s) * 16, v[s]);
+            }
+            umma::wait_st();
+            umma::fence_before();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&made[q]);
+                mbar_arrive(&used[st]);
+            }
         }
     } else {
         // row sr of the two panels, columns n0 ..
@@ -375,7 +403,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == 0) umma::dealloc(tm, 2 * NPAD);
+    if (warp == 0) umma::dealloc(tm, 512);
 }
 
 // One block per (sequence, panel): turns the segments' end states from zero into their

@@ -177,6 +177,22 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16])
         : "memory");
 }
 
+// 16 lanes (from the address's lane) x 16 columns, as four 8 x 8 bf16 tiles read by
+// ldsm_t leave them: registers 2 q, 2 q + 1 hold lanes l / 4 and l / 4 + 8, column 4 q + l % 4.
+__device__ __forceinline__ void st_tiles(uint32_t addr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// Four 8 x 8 bf16 tiles, transposed: lane l of tile i gives the address of the tile's row
+// l % 8 (lanes 8 i ..), and gets column l / 4, rows 2 (l % 4) and + 1.
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+
 // Two fp32 to a bf16 pair, lo in the low half.
 __device__ __forceinline__ uint32_t pack(float lo, float hi)
 {
