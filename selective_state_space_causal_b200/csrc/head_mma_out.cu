@@ -12,6 +12,8 @@
 // e^{c_t - c_s} needs no exponential per pair below the diagonal blocks: for t in the
 // 32-token block i and s in an earlier one it is e^{c_t - r_i} e^{r_i - c_s}, r_i the
 // running sum before block i, and both factors are at most one.
+#include <type_traits>
+
 #include "head_mma.cuh"
 
 namespace ssm {
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kOutThreads) head_out_kernel(OutArgs a, const 
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    const uint32_t tm = tmem_slot;
+    constexpr uint32_t tm = umma::kWhole;
     const uint32_t tM = tm + 128 + team * 192, tYa = tM + 64, tYb = tM + 128;
     const int p0 = pb + team, count = p0 < pe ? (pe - p0 + kTeams - 1) / kTeams : 0;
     bool failed = false;
@@ -138,30 +140,38 @@ __global__ void __launch_bounds__(kOutThreads) head_out_kernel(OutArgs a, const 
         __syncwarp();
     } else if (warp >= kOutIssuer) {
         if (umma::elect()) {
+            const uint64_t c0 = umma::desc_k(sC, 0), b0 = umma::desc_k(sB, 0);
+            auto c_at = [](int k) { return (uint32_t)(k / 4 * umma::kPanel + k % 4 * 32); };
             if (team == 0) {
 #pragma unroll
                 for (int k = 0; k < NPAD / 16; ++k)
-                    umma::mma(tm, umma::desc_k(sC + (k / 4) * umma::kPanel, k % 4),
-                              umma::desc_k(sB + (k / 4) * umma::kPanel, k % 4), umma::idesc(128, false, false),
+                    umma::mma(tm, umma::moved(c0, c_at(k)), umma::moved(b0, c_at(k)), umma::idesc(128, false, false),
                               k > 0);
                 umma::commit(&gbar);
             }
-            for (int it = 0; it < count; ++it) {
-                const uint32_t su = sW + (it & 1) * STAGE, ss = su + umma::kPanel;
-                wait(&landed[team][it & 1], it >> 1);
-                if (it > 0) wait(&stored[team][(it - 1) & 1], (it - 1) >> 1);  // both accumulators were read
-                umma::fence_after();
+            const uint64_t u0 = umma::desc_mn(sW, 0, 0), s0 = umma::plain_k(sW + umma::kPanel, 0, 64);
+            auto run = [&](auto which) {  // the team's columns, known when compiling
+                constexpr uint32_t m = tm + 128 + decltype(which)::value * 192, ya = m + 64, yb = m + 128;
+                for (int it = 0; it < count; ++it) {
+                    const uint32_t at = (it & 1) * STAGE;
+                    const uint64_t u = umma::moved(u0, at), s = umma::moved(s0, at);
+                    wait(&landed[team][it & 1], it >> 1);
+                    if (it > 0) wait(&stored[team][(it - 1) & 1], (it - 1) >> 1);  // both accumulators were read
+                    umma::fence_after();
 #pragma unroll
-                for (int k = 0; k < NPAD / 16; ++k)
-                    umma::mma(tYb, umma::desc_k(sC + (k / 4) * umma::kPanel, k % 4), umma::plain_k(ss, k, 64),
-                              umma::idesc(64, false, false), k > 0);
-                wait(&ready[team], it);
-                umma::fence_after();
+                    for (int k = 0; k < NPAD / 16; ++k)
+                        umma::mma(yb, umma::moved(c0, c_at(k)), umma::moved(s, k * 2048), umma::idesc(64, false, false),
+                                  k > 0);
+                    wait(&ready[team], it);
+                    umma::fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    umma::mma_ta(tYa, tM + 8 * k, umma::desc_mn(su, k, 0), umma::idesc(64, false, true), k > 0);
-                umma::commit(&done[team]);
-            }
+                    for (int k = 0; k < 8; ++k)
+                        umma::mma_ta(ya, m + 8 * k, umma::moved(u, k * 2048), umma::idesc(64, false, true), k > 0);
+                    umma::commit(&done[team]);
+                }
+            };
+            if (team == 0) run(std::integral_constant<uint32_t, 0>());
+            else run(std::integral_constant<uint32_t, 1>());
         }
         __syncwarp();
     } else {

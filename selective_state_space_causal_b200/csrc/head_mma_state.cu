@@ -8,6 +8,8 @@
 // state keeps fp32 accuracy; b is bf16 as given. The products of different chunks are
 // independent: only S' = e S + delta runs chunk after chunk, in registers, while the
 // next products are under way.
+#include <type_traits>
+
 #include "head_mma.cuh"
 
 namespace ssm {
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    const uint32_t tm = tmem_slot, planes = tm + 256;  // two products, then 4 x 3 planes of 16 columns
+    constexpr uint32_t tm = umma::kWhole, planes = tm + 256;  // two products, then 4 x 3 planes of 16 columns
     bool failed = false;
     auto chunk_at = [&](int kk) { return REV ? nchunk - 1 - kk : kk; };
     auto len_of = [&](int k) { return min(kC, sg.len - k * kC); };
@@ -215,10 +217,14 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
         }
     } else if (warp == kIssuer) {
         if (umma::elect()) {
-            for (int kk = 0; kk < nchunk; ++kk) {
-                const uint32_t sb = stages + kk % kStages * STAGE + 2 * umma::kPanel, d = tm + (kk & 1) * NPAD;
-                wait(&landed[kk % kStages], kk / kStages);
-                if (kk >= 2) wait(&taken[kk & 1], (kk >> 1) - 1);
+            const uint64_t b0 = umma::desc_mn(stages + 2 * umma::kPanel, 0, umma::kPanel);
+            int st = 0, round = 0;
+            auto chunk = [&](int kk, auto buf) {
+                constexpr uint32_t d = tm + decltype(buf)::value * NPAD;
+                const uint64_t b = umma::moved(b0, st * STAGE);
+                wait(&landed[st], round);
+                if (kk >= 2) wait(&taken[decltype(buf)::value], (kk >> 1) - 1);
+#pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     wait(&made[q], kk);
                     umma::fence_after();
@@ -226,13 +232,20 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
                     for (int s = 0; s < 3; ++s)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            umma::mma_ta(d, planes + (3 * q + s) * 16 + 8 * k,
-                                         umma::desc_mn(sb, 2 * q + k, umma::kPanel), umma::idesc(NPAD, false, true),
-                                         q + s + k > 0);
+                            umma::mma_ta(d, planes + (3 * q + s) * 16 + 8 * k, umma::moved(b, (2 * q + k) * 2048),
+                                         umma::idesc(NPAD, false, true), q + s + k > 0);
                     umma::commit(&eaten[q]);
                 }
-                umma::commit(&summed[kk & 1]);
-                umma::commit(&used[kk % kStages]);
+                umma::commit(&summed[decltype(buf)::value]);
+                umma::commit(&used[st]);
+                if (++st == kStages) {
+                    st = 0;
+                    ++round;
+                }
+            };
+            for (int kk = 0; kk < nchunk; kk += 2) {
+                chunk(kk, std::integral_constant<uint32_t, 0>());
+                if (kk + 1 < nchunk) chunk(kk + 1, std::integral_constant<uint32_t, 1>());
             }
         }
         __syncwarp();
@@ -289,7 +302,6 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
             }
             umma::wait_st();
             umma::fence_before();
-            fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&made[q]);

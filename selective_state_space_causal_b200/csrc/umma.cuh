@@ -54,6 +54,10 @@ __device__ __forceinline__ uint64_t plain_mn(uint32_t tile, int k16, int rows)
     return desc_plain(tile + k16 * 256, 128, 16 * rows);
 }
 
+// A descriptor moved on by `bytes`: cheap enough to be an immediate, where building each
+// descriptor anew costs an issuing thread more than the instruction itself.
+__device__ __forceinline__ constexpr uint64_t moved(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 128.
 __device__ __forceinline__ constexpr uint32_t idesc(int N, bool a_mn, bool b_mn)
 {
@@ -97,6 +101,10 @@ __device__ __forceinline__ void commit(uint64_t *bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  :: "r"(saddr(bar)) : "memory");
 }
+
+// A CTA that allocates all 512 columns gets them from column 0: with addresses known when
+// compiling, an issuing thread needs no registers moved to the uniform file.
+constexpr uint32_t kWhole = 0;
 
 // One warp: allocate / free `cols` (a power of two >= 32) columns of tensor memory.
 __device__ __forceinline__ void alloc(uint32_t *slot, uint32_t cols)
