@@ -25,6 +25,7 @@ int64_t noalloc_max_sequences();
 int read_replay_status(bool clear);
 int read_head_state_status(bool clear);
 int read_head_out_status(bool clear);
+int read_head_bwd_status(bool clear);
 int probe_sink_floats();
 int read_selftest_status(bool clear);
 cudaError_t launch_wait_selftest(unsigned tries, cudaStream_t stream, int *launches);
@@ -210,7 +211,8 @@ int ssm_device_status(int clear)
     const int a1 = ssm::read_conv_scan_status(clear != 0);
     const int a2 = ssm::read_head_state_status(clear != 0);
     const int a3 = ssm::read_head_out_status(clear != 0);
-    const int a = (a0 < 0 || a1 < 0 || a2 < 0 || a3 < 0) ? -1 : (a0 | a1 | a2 | a3);
+    const int a4 = ssm::read_head_bwd_status(clear != 0);
+    const int a = (a0 < 0 || a1 < 0 || a2 < 0 || a3 < 0 || a4 < 0) ? -1 : (a0 | a1 | a2 | a3 | a4);
     const int b = ssm::read_conv_status(clear != 0);
     const int d = ssm::read_decode_status(clear != 0);
     const int r = ssm::read_replay_status(clear != 0);

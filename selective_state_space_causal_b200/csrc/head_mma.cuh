@@ -9,7 +9,9 @@
 // its value before 32-token block i,
 //   d      d_t                      l      c_t - r_{block of t}
 //   ec     2^{c_t}                  wf     d_t 2^{c_127 - c_t}
-//   col    d_t 2^{r_i - c_t} for blocks i = 1..3 and t < 32 i (192 values)
+//   col    2^{r_i - c_t} for blocks i = 1..3 and t < 32 i (192 values); times d_t in
+//          the forward's tables
+//   wn, el 2^{c_127 - c_t} and 2^{l_t}, for the backward
 #pragma once
 
 #include "head_scan.cuh"
@@ -46,7 +48,8 @@ __device__ __forceinline__ PanelRef panel_of(const Dims &z, int g, int pi)
 
 // Tables of one (chunk slot, head), in floats.
 constexpr int kTabD = 0, kTabL = kC, kTabEc = 2 * kC, kTabCol = 3 * kC, kTabWf = 3 * kC + 192;
-constexpr int kTab = 4 * kC + 192;
+constexpr int kTabWn = kTabWf + kC, kTabEl = kTabWn + kC;
+constexpr int kTab = 6 * kC + 192;
 constexpr int kTabOut = kTabWf;  // what the outputs need comes first
 __host__ __device__ constexpr int col_at(int i) { return kTabCol + (i == 1 ? 0 : i == 2 ? 32 : 96); }
 
@@ -156,8 +159,8 @@ struct StateArgs {
 };
 
 // Steps and running decays of every chunk.
-cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, cudaStream_t stream,
-                          int *launches);
+cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, bool backward,
+                          cudaStream_t stream, int *launches);
 // The states before every chunk (forward) or the gradients of the states after every
 // chunk (reverse), `planes` bf16 planes each.
 cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, bool vec,
@@ -168,6 +171,8 @@ Dims dims_of(const HeadScanArgs &a);
 // Tokens per segment of the walk, and whether walks are split.
 int64_t segment_span(const Dims &z, bool *split);
 
+cudaError_t launch_backward(const HeadScanArgs &a, cudaStream_t stream, int *launches);
+size_t backward_bytes(const Dims &z);
 cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t stream, int *launches);
 size_t forward_bytes(const Dims &z);
 
@@ -177,4 +182,8 @@ inline bool vec16(const void *p, int64_t stride, int64_t width)
 }
 
 }  // namespace hm
+
+// Sums of the chunks' shares (slot, head, 3) of dA, ddt_bias and dDskip, in a fixed order.
+cudaError_t launch_head_reduce(const float *part, int64_t slots, int H, float *dA, float *dbias,
+                               float *dskip, cudaStream_t stream, int *launches);
 }  // namespace ssm

@@ -328,7 +328,7 @@ cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t st, int *launches
     char *ws = static_cast<char *>(a.workspace);
     float *tab = reinterpret_cast<float *>(ws + l.tab);
     bf16 *marks = reinterpret_cast<bf16 *>(ws + l.marks);
-    if (cudaError_t e = launch_tables(a, z, tab, st, launches); e != cudaSuccess) return e;
+    if (cudaError_t e = launch_tables(a, z, tab, false, st, launches); e != cudaSuccess) return e;
     const bool vec = vec16(a.B, a.bc_stride, a.N) && vec16(a.C, a.bc_stride, a.N) && vec16(a.u, a.u_stride, a.P);
     StateArgs s{z, static_cast<const bf16 *>(a.u), a.u_stride, static_cast<const bf16 *>(a.B), a.bc_stride,
                 tab, a.h0, a.h_final, marks, span, reinterpret_cast<float *>(ws + l.seg),

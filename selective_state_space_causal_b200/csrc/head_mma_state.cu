@@ -22,7 +22,7 @@ namespace {
 // One block per (chunk slot, 32 heads).
 __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *delta, int64_t stride,
                                                          const float *A, const float *bias,
-                                                         int softplus, float *tab)
+                                                         int softplus, bool backward, float *tab)
 {
     __shared__ float sd[kC][33];
     const int64_t slot = blockIdx.x;
@@ -63,16 +63,19 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
         pre -= sum;
         const int blk = lane / 8;
         const double r = blk == 0 ? 0.0 : blk == 1 ? r1 : blk == 2 ? r2 : r3;
-        float lv[4], ev[4], wv[4], c1[4], c2[4], c3[4];
+        float lv[4], ev[4], wv[4], wn[4], el[4], c1[4], c2[4], c3[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const double c = pre + run[j];
             lv[j] = (float)(c - r);
             ev[j] = ex2_approx((float)c);
-            wv[j] = dv[j] * ex2_approx((float)(last - c));
-            c1[j] = dv[j] * ex2_approx((float)(r1 - c));
-            c2[j] = dv[j] * ex2_approx((float)(r2 - c));
-            c3[j] = dv[j] * ex2_approx((float)(r3 - c));
+            wn[j] = ex2_approx((float)(last - c));
+            wv[j] = dv[j] * wn[j];
+            el[j] = ex2_approx(lv[j]);
+            const float f = backward ? 1.0f : dv[j];
+            c1[j] = f * ex2_approx((float)(r1 - c));
+            c2[j] = f * ex2_approx((float)(r2 - c));
+            c3[j] = f * ex2_approx((float)(r3 - c));
         }
         float *q = tab + (slot * z.H + h0 + i) * kTab;
         auto put = [&](int at, const float (&v)[4]) {
@@ -82,6 +85,10 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
         put(kTabL, lv);
         put(kTabEc, ev);
         put(kTabWf, wv);
+        if (backward) {
+            put(kTabWn, wn);
+            put(kTabEl, el);
+        }
         if (blk < 1) put(col_at(1), c1);
         if (blk < 2) put(col_at(2), c2);
         if (blk < 3) put(col_at(3), c3);
@@ -522,12 +529,12 @@ int64_t segment_span(const Dims &z, bool *split)
     return seg * kC;
 }
 
-cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, cudaStream_t stream,
-                          int *launches)
+cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, bool backward,
+                          cudaStream_t stream, int *launches)
 {
     const dim3 grid((unsigned)head_slots(z.tok, z.S, kC), (unsigned)((z.H + 31) / 32));
     head_table_kernel<<<grid, 256, 0, stream>>>(z, static_cast<const bf16 *>(a.delta), a.delta_stride,
-                                                a.A, a.dt_bias, a.delta_softplus, tab);
+                                                a.A, a.dt_bias, a.delta_softplus, backward, tab);
     ++*launches;
     return cudaGetLastError();
 }

@@ -549,12 +549,18 @@ cudaError_t bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
     head_bwd_chunk_kernel<T><<<dim3((unsigned)slots, (unsigned)a.G), 256, bytes, stream>>>(b);
     ++*launches;
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    head_reduce_kernel<<<(unsigned)a.H, 256, 0, stream>>>(part, slots, b.H, a.dA, a.ddt_bias, a.dDskip);
-    ++*launches;
-    return cudaGetLastError();
+    return launch_head_reduce(part, slots, b.H, a.dA, a.ddt_bias, a.dDskip, stream, launches);
 }
 
 }  // namespace
+
+cudaError_t launch_head_reduce(const float *part, int64_t slots, int H, float *dA, float *dbias,
+                               float *dskip, cudaStream_t stream, int *launches)
+{
+    head_reduce_kernel<<<(unsigned)H, 256, 0, stream>>>(part, slots, H, dA, dbias, dskip);
+    ++*launches;
+    return cudaGetLastError();
+}
 
 size_t head_scan_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N, int64_t S,
                                  DType dtype)
@@ -568,6 +574,11 @@ size_t head_scan_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, i
 size_t head_scan_bwd_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
                                      int64_t S, DType dtype)
 {
+    if (dtype == DType::BF16) {
+        HeadScanArgs a{};
+        a.S = S; a.tok = tok; a.H = H; a.P = P; a.G = G; a.N = N;
+        return hm::backward_bytes(hm::dims_of(a));
+    }
     const int64_t slots = head_slots(tok, S, kQ);
     return 2 * align256((size_t)slots * H * P * N * 4) + align256((size_t)slots * H * 3 * 4);
 }
@@ -580,7 +591,7 @@ cudaError_t launch_head_scan(const HeadScanArgs &a, cudaStream_t stream, int *la
 
 cudaError_t launch_head_scan_bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 {
-    return a.dtype == DType::BF16 ? bwd<__nv_bfloat16>(a, stream, launches)
+    return a.dtype == DType::BF16 ? hm::launch_backward(a, stream, launches)
                                   : bwd<float>(a, stream, launches);
 }
 

@@ -5,13 +5,18 @@ Bounds. The kernels keep states, decays and sums in fp32. With fp32 activations 
 product and sum is fp32 too: a sum of n terms of like size is off by about
 sqrt(n) 2^-24 of its own size (n <= a few thousand here, so below 4e-6), a decay's
 exponent by 2^-24 of its size (below 1e-5 at exponents of 100); 1e-4 of the tensor's
-rms covers both. With bf16 activations the weights of a product inside a chunk are
-rounded to bf16 once: each term is off by at most 2^-8 of itself, their sum by about
-2^-8 / sqrt(3) of its rms (2^-8 |value| in the worst case of equal signs, which the
-half step below covers), so 2e-2 of the rms is far above it; values stored in bf16
-get half a step, 2^-8 |value|, on top. Outputs kept in fp32 (states, gradients of A,
-of the biases and of D) are products of the rounded inputs, not rounded again, and
-are held to 1e-4.
+rms covers both.
+
+With bf16 activations one factor of each product is rounded to bf16 once: inside a
+chunk of 128 tokens the weights M = (C.B) decay d (for y and du) or dM decay d (for dB
+and dC), across chunks the state that a chunk starts from (or its gradient). bf16 keeps
+8 bits, so a rounded factor is off by at most 2^-8 of itself, and a sum of products
+with it by at most 2^-8 of the sum of the products' sizes, which `sizes` computes
+element by element. A value stored in bf16 is off by half a step on top, 2^-8 of it.
+(A fixed fraction of the tensor's rms is no bound: heads with large steps d have
+outputs, and so roundings, many times the rms.) Outputs kept in fp32 (states,
+gradients of A, of the biases and of D) are products of the given inputs and unrounded
+weights, and are held to 1e-4.
 """
 
 import numpy as np
@@ -98,6 +103,51 @@ def scan_bwd(u, delta, A, B, C, D, bias, sp, h0, lens, dy, dhf):
     return g
 
 
+CHUNK = 128
+
+
+def sizes(u, delta, A, B, C, D, bias, sp, h0, lens, dy=None, dhf=None):
+    """Per element, the sum of the sizes of the products with one rounded factor."""
+    tok, H, P = u.shape
+    G, N = B.shape[1:]
+    rep = H // G
+    raw = delta + (bias if bias is not None else 0.0)
+    d = softplus(raw) if sp else raw
+    out = {"y": torch.zeros_like(u), "du": torch.zeros_like(u), "dB": torch.zeros_like(B), "dC": torch.zeros_like(C)}
+    for s, (lo, hi) in enumerate(bounds_of(lens)):
+        cuts = [(a, min(a + CHUNK, hi)) for a in range(lo, hi, CHUNK)]
+        per = []
+        h = h0[s] if h0 is not None else torch.zeros((H, P, N), dtype=F64)
+        for a, b in cuts:
+            dc = d[a:b].t()                                   # (H, Q)
+            c = torch.cumsum(dc * A[:, None], 1)
+            Bh, Ch = (x[a:b].repeat_interleave(rep, 1).transpose(0, 1) for x in (B, C))  # (H, Q, N)
+            uh = u[a:b].transpose(0, 1)
+            L = torch.exp(c[:, :, None] - c[:, None, :]).tril() * dc[:, None, :]
+            w = dc * torch.exp(c[:, -1:] - c)
+            per.append((a, b, c, Bh, Ch, uh, L, w, h))
+            h = torch.exp(c[:, -1])[:, None, None] * h + (w[..., None] * uh).transpose(1, 2) @ Bh
+        for a, b, c, Bh, Ch, uh, L, w, h in per:
+            M = (Ch @ Bh.transpose(1, 2)).abs() * L
+            e = torch.exp(c)[..., None]
+            out["y"][a:b] = (M @ uh.abs() + e * (Ch.abs() @ h.abs().transpose(1, 2))).transpose(0, 1)
+        if dy is None:
+            continue
+        g = dhf[s] if dhf is not None else torch.zeros((H, P, N), dtype=F64)
+        for a, b, c, Bh, Ch, uh, L, w, h in reversed(per):
+            yh = dy[a:b].transpose(0, 1)
+            e = torch.exp(c)[..., None]
+            M = (Ch @ Bh.transpose(1, 2)).abs() * L
+            out["du"][a:b] = (M.transpose(1, 2) @ yh.abs()).transpose(0, 1)
+            X = (yh @ uh.transpose(1, 2)).abs() * L
+            dC = X @ Bh.abs() + e * (yh.abs() @ h.abs())
+            dB = X.transpose(1, 2) @ Ch.abs() + w[..., None] * (uh.abs() @ g.abs())
+            for k, v in (("dC", dC), ("dB", dB)):
+                out[k][a:b] = v.view(G, rep, b - a, N).sum(1).transpose(0, 1)
+            g = torch.exp(c[:, -1])[:, None, None] * g + (e * yh).transpose(1, 2) @ Ch
+    return out
+
+
 def norm(v, group, eps):
     vg = v.reshape(v.shape[0], v.shape[1] // group, group)
     return (vg / torch.sqrt((vg * vg).mean(-1, keepdim=True) + eps)).reshape(v.shape)
@@ -109,8 +159,9 @@ def gated(x, z, w, group, eps, before):
     return y * w if w is not None else y
 
 
-def worst(gpu, ref, stored_bf16, tol):
-    """Largest error over its bound: tol * rms(ref), plus half a bf16 step where stored so."""
+def worst(gpu, ref, stored_bf16, tol, size=None):
+    """Largest error over its bound: tol * rms(ref), plus half a bf16 step where stored so,
+    plus 2^-8 of `size` where a factor was rounded."""
     g, r = gpu.detach().double().cpu().numpy(), ref.detach().double().numpy()
     assert g.shape == r.shape, (g.shape, r.shape)
     if r.size == 0:
@@ -119,9 +170,11 @@ def worst(gpu, ref, stored_bf16, tol):
         return float("inf")
     rms = float(np.sqrt(np.mean(r * r)))
     off = np.abs(g - r) - (2.0 ** -8 * np.abs(r) if stored_bf16 else 0.0)
+    if size is not None:  # the half step is of the rounded value: 2^-8 (|r| + its error)
+        off = off - 2.0 ** -8 * (1 + 2.0 ** -8) * size.numpy()
     return float(off.max()) / (tol * rms if rms else tol)
 
 
-def close(gpu, ref, stored_bf16, tol, what):
-    w = worst(gpu, ref, stored_bf16, tol)
+def close(gpu, ref, stored_bf16, tol, what, size=None):
+    w = worst(gpu, ref, stored_bf16, tol, size)
     assert w <= 1.0, f"{what}: error is {w:.3g} x the bound"

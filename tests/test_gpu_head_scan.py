@@ -1,5 +1,5 @@
 """The scan with one decay per head on the GPU: forward, backward, one decode token,
-against the plain 64-bit forms of head_oracle.py."""
+against the plain 64-bit forms of head_oracle.py, with the bounds derived there."""
 
 import pytest
 import torch
@@ -10,10 +10,6 @@ import selective_state_space_causal_b200 as ssm
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
-
-
-def tol_of(dt):
-    return 2e-2 if dt == BF else 1e-4
 
 
 class Case:
@@ -93,15 +89,22 @@ class Case:
                               cu_seqlens=None if dense else self.cu, S=S, workspace=self.ws(True))
         return g
 
+    def size(self, bwd=False):
+        """The sizes that bf16 roundings go by (None: nothing is rounded)."""
+        if self.dt != BF:
+            return {}
+        return ho.sizes(*self.ref_args(), *((self.dy.double(), self.f(self.dhf)) if bwd else ()))
+
     def check_fwd(self, y, hf):
         ry, rh = ho.scan(*self.ref_args())
-        ho.close(y, ry, self.dt == BF, tol_of(self.dt), "y")
+        ho.close(y, ry, self.dt == BF, 1e-4, "y", self.size().get("y"))
         ho.close(hf, rh, False, 1e-4, "h_final")
 
     def check_bwd(self, g):
         r = ho.scan_bwd(*self.ref_args(), self.dy.double(), self.f(self.dhf))
+        size = self.size(bwd=True)
         for k in ("du", "ddelta", "dB", "dC"):
-            ho.close(g[k], r[k], self.dt == BF, tol_of(self.dt), k)
+            ho.close(g[k], r[k], self.dt == BF, 1e-4, k, size.get(k))
         ho.close(g["dh0"], r["dh0"], False, 1e-4, "dh0")
         # sums over tokens: against the size of what is summed, which their rounding goes by
         for k, size in (("dA", r["dA_size"]), ("ddt_bias", r["dbias_size"])):
@@ -200,8 +203,9 @@ def test_sequences_do_not_touch_each_other(dt):
     assert (y3[100:] == 3.0).all()
     c.lens = [70, 30]
     c.u, c.delta, c.B, c.C = c.u[:100], c.delta[:100], c.B[:100], c.C[:100]
+    c.h0 = c.h0[:2]
     ry, _ = ho.scan(*c.ref_args())
-    ho.close(y3[:100], ry, dt == BF, tol_of(dt), "y")
+    ho.close(y3[:100], ry, dt == BF, 1e-4, "y", c.size().get("y"))
 
 
 @pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
@@ -218,7 +222,21 @@ def test_chunks_carry_the_state(dt):
                               Dskip=c.g(c.D), dt_bias=c.g(c.bias), h0=h, h_final=h,
                               workspace=torch.empty(max(n, 1), dtype=torch.uint8, device="cuda"))
         ys.append(y)
-    c.check_fwd(torch.cat(ys), h)
+    # chunks start with each call, so the calls' own roundings are the sizes of three sequences
+    ry, rh = ho.scan(*c.ref_args())
+    size = None
+    if dt == BF:
+        parts, start = [], c.f(c.h0)
+        for lo, hi in ((0, 256), (256, 301), (301, 700)):
+            a = list(c.ref_args())
+            for i in (0, 1, 3, 4):
+                a[i] = a[i][lo:hi]
+            a[8], a[9] = start, [hi - lo]
+            parts.append(ho.sizes(*a)["y"])
+            start = ho.scan(*a)[1]
+        size = torch.cat(parts)
+    ho.close(torch.cat(ys), ry, dt == BF, 1e-4, "y", size)
+    ho.close(h, rh, False, 1e-4, "h_final")
 
 
 @pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
@@ -286,7 +304,8 @@ def test_prompt_then_tokens(dt):
             dst.copy_(src[T + i:T + i + 1])
         graph.replay()
         ys.append(y1.clone())
-    ho.close(torch.cat(ys), ry, dt == BF, tol_of(dt), "y")
+    # the prompt's chunks are the whole text's, and a token by itself rounds nothing
+    ho.close(torch.cat(ys), ry, dt == BF, 1e-4, "y", c.size().get("y"))
     ho.close(h, rh[0:1], False, 1e-4, "state")
 
 

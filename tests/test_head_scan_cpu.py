@@ -179,6 +179,33 @@ def test_chunk_slots_are_distinct_and_found_again(span):
             assert found == used.get(slot)
 
 
+def test_sizes_bound_what_a_rounded_factor_does():
+    """Rounding M, or the state a chunk starts from, by up to 2^-8 moves y by at most 2^-8
+    of `sizes`: shown on the matrix form with random roundings."""
+    g = torch.Generator().manual_seed(5)
+    lens, H, P, G, N = [150], 2, 4, 1, 6
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    u, delta, B, C, h0 = r(150, H, P), r(150, H), r(150, G, N), r(150, G, N), r(1, H, P, N)
+    A = -torch.rand(H, generator=g, dtype=torch.float64)
+    y, _ = ho.scan(u, delta, A, B, C, None, None, True, h0, lens)
+    size = ho.sizes(u, delta, A, B, C, None, None, True, h0, lens)["y"]
+    d = ho.softplus(delta)
+    got = torch.zeros_like(y)
+    h = h0[0]
+    for a, b in ((0, 128), (128, 150)):
+        c = torch.cumsum(d[a:b] * A, 0).t()
+        L = torch.exp(c[:, :, None] - c[:, None, :]).tril() * d[a:b].t()[:, None, :]
+        Bh, Ch, uh = B[a:b, 0], C[a:b, 0], u[a:b].transpose(0, 1)
+        M = (Ch @ Bh.t()) * L
+        M = M * (1 + (2 * torch.rand(M.shape, generator=g, dtype=torch.float64) - 1) * 2.0 ** -8)
+        hr = h * (1 + (2 * torch.rand(h.shape, generator=g, dtype=torch.float64) - 1) * 2.0 ** -8)
+        got[a:b] = (M @ uh + torch.exp(c)[..., None] * (Ch @ hr.transpose(1, 2))).transpose(0, 1)
+        w = d[a:b].t() * torch.exp(c[:, -1:] - c)
+        h = torch.exp(c[:, -1])[:, None, None] * h + (w[..., None] * uh).transpose(1, 2) @ Bh
+    off = (got - y).abs()
+    assert (off <= 2.0 ** -8 * size + 1e-12).all() and off.max() > 2.0 ** -12
+
+
 @pytest.mark.parametrize("sp", [True, False])
 def test_written_out_gradients_match_autograd_and_differences(sp):
     g = torch.Generator().manual_seed(0)
