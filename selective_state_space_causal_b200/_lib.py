@@ -402,26 +402,24 @@ class _NormScalars(ctypes.Structure):
 
 def _token_stride(t, what: str) -> int:
     """Elements between tokens of a (tok, ...) tensor whose tokens are contiguous rows."""
-    width = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != width:
+    shape, stride, width = t.shape, t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != width and shape[i] != 1:
             raise SsmError(-1, f"{what}: the dimensions after the first must be contiguous")
-        width *= size
-    return t.stride(0) if t.shape[0] > 1 else width
+        width *= shape[i]
+    return stride[0] if shape[0] > 1 else width
 
 
 def _shared_stride(B, C) -> int:
     b, c = _token_stride(B, "B"), _token_stride(C, "C")
-    if B.shape != C.shape or b != c:
+    if b != c or B.shape != C.shape:
         raise SsmError(-1, "B and C must have the same shape and token stride")
     return b
 
 
 def _same(what: str, t, dtype, shape) -> None:
     """A contiguous tensor of this dtype and shape, or None."""
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
         raise SsmError(-1, f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
                            f"got {t.dtype} {tuple(t.shape)}")
 
@@ -434,7 +432,7 @@ def _head_shapes(u, delta, A, B, C, Dskip, dt_bias):
         raise SsmError(-1, "u must be (tok, H, P), B and C (tok, G, N)")
     tok, H, P = u.shape
     _, G, N = B.shape
-    if B.shape[0] != tok or tuple(delta.shape) != (tok, H):
+    if B.shape[0] != tok or delta.shape != (tok, H):
         raise SsmError(-1, "u, delta, B and C must have the same tokens, delta one column per head")
     if not (u.dtype == delta.dtype == B.dtype == C.dtype):
         raise SsmError(-2, "u, delta, B and C must have one dtype")
@@ -460,8 +458,14 @@ def _on_gpu(*tensors) -> None:
     """Every tensor on the current CUDA device: the kernels run there, on its stream."""
     import torch
 
+    here = None
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+        if t is None:
+            continue
+        d = t.get_device()  # -1: host memory
+        if here is None and d >= 0:
+            here = torch.cuda.current_device()
+        if d < 0 or d != here:
             raise SsmError(-1, f"a tensor is on {t.device}, not on the current CUDA device")
 
 
@@ -522,8 +526,7 @@ def ssm_head_scan_bwd(u, delta, A, B, C, dy, grads, Dskip=None, dt_bias=None, de
             ("dDskip", g.get("dDskip"), f32, (H,)), ("ddt_bias", g.get("ddt_bias"), f32, (H,)),
             ("dh0", g.get("dh0"), f32, (S, H, P, N))):
         _same(name, t, dt, shape)
-        _on_gpu(t)
-    _on_gpu(u, delta, A, B, C, Dskip, dt_bias, h0, dh_final, cu_seqlens, workspace)
+    _on_gpu(u, delta, A, B, C, Dskip, dt_bias, h0, dh_final, cu_seqlens, workspace, dy, *g.values())
     _check(lib.ssm_head_scan_bwd(
         _ptr(u), _token_stride(u, "u"), _ptr(delta), _token_stride(delta, "delta"), _ptr(A), _ptr(B),
         _ptr(C), _shared_stride(B, C), _ptr(Dskip), _ptr(dt_bias), int(bool(delta_softplus)),
@@ -588,8 +591,7 @@ def ssm_gated_norm_bwd(x, dy, grads, weight=None, z=None, group_size=None, eps=1
     _same("dweight", grads.get("dweight"), torch.float32, (D,))
     for name, t in (("dy", dy), ("dx", grads["dx"]), ("dz", grads.get("dz"))):
         _same(name, t, x.dtype, (tok, D))
-        _on_gpu(t)
-    _on_gpu(x, z, weight, grads.get("dweight"), workspace)
+    _on_gpu(x, z, weight, dy, workspace, *grads.values())
     sc = _NormScalars(eps, 1.0)
     _check(lib.ssm_gated_norm_bwd(
         _ptr(x), _token_stride(x, "x"), _ptr(z), D if z is None else _token_stride(z, "z"),
@@ -639,8 +641,7 @@ def ssm_residual_norm_bwd(r, dy, grads, x=None, weight=None, x_scale=None, alpha
             ("dweight", g.get("dweight"), torch.float32, (D,)),
             ("dx_scale", g.get("dx_scale"), torch.float32, (D,))):
         _same(name, t, dt, shape)
-        _on_gpu(t)
-    _on_gpu(workspace)
+    _on_gpu(r, x, dy, dresidual_out, weight, x_scale, workspace, *g.values())
     sc = _NormScalars(eps, alpha)
     _check(lib.ssm_residual_norm_bwd(
         _ptr(r), _ptr(x), _ptr(x_scale), _ptr(weight), ctypes.addressof(sc), _ptr(dy),

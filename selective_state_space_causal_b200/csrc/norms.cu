@@ -8,10 +8,12 @@
 //   dv = rstd (dh - vh mean(dh vh)),  dw = sum over rows of dy vh (times the gate).
 //
 // All four are bound by memory: every input is read once and every output written
-// once, because a team of threads (a warp for groups up to 256 vectors, a block
-// beyond) keeps its row in registers between the sum and the scaling. Vectors are 16
-// bytes. Rows that are not 16-byte aligned, or longer than the registers hold, go to
-// kernels that read the row twice (the second time from cache).
+// once, because a team of threads (a warp for groups up to 64 vectors, a block sized to
+// the row beyond) keeps its row in registers between the sums and the scaling. The
+// backward keeps the row as it was loaded, computes from it twice, and loads the next
+// row before it waits for this one's sums. Vectors are 16 bytes of activations. Rows
+// that are not 16-byte aligned, or longer than the registers hold, go to kernels that
+// read the row twice (the second time from cache).
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,18 +40,24 @@ __device__ __forceinline__ float sigmoid_of(float z, __nv_bfloat16)
     return __fdividef(1.0f, 1.0f + __expf(-z));  // inf in the denominator gives 0
 }
 
-template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float *sm)
+// Sums of a team's values in every thread of it: a warp, or (WARP false) the block. A
+// block's calls take the two halves of sm in turn, so one barrier a call is enough.
+template <bool WARP>
+__device__ __forceinline__ float2 team_sum(float2 v, float2 (*sm)[32], int turn)
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if constexpr (TEAM > 32) {
-        __syncthreads();  // sm may still be read from the call before
-        if ((threadIdx.x & 31) == 0) sm[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < TEAM / 32; ++i) v += sm[i];
+    for (int o = 16; o; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if (WARP) return v;
+    float2 *buf = sm[turn & 1];
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+        v.x += buf[i].x;
+        v.y += buf[i].y;
     }
     return v;
 }
@@ -100,14 +108,15 @@ __device__ __forceinline__ void store_f(T *p, const float (&v)[V])
 template <typename T> struct VecOf { static constexpr int v = 16 / sizeof(T); };
 
 // MODE 0: x only; 1: gate then norm; 2: norm then gate; 3: residual.
-template <typename T, typename R, int MODE, int TEAM, int K>
-__global__ void __launch_bounds__(256) norm_fwd_kernel(Args a)
+template <typename T, typename R, int MODE, bool WARP, int K>
+__global__ void __launch_bounds__(WARP ? 256 : 512) norm_fwd_kernel(Args a)
 {
     constexpr int V = VecOf<T>::v;
-    __shared__ float sm[8];
-    const int l = threadIdx.x % TEAM;
-    const int64_t row = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM;
-    if (TEAM == 32 && row >= a.tok) return;  // a block-wide team always has a row
+    __shared__ float2 sm[2][32];
+    const int TEAM = WARP ? 32 : blockDim.x;
+    const int l = WARP ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
+    if (WARP && row >= a.tok) return;  // a block always has a row
     const int gs = a.group, c0 = blockIdx.y * gs;
     const T *x = static_cast<const T *>(a.x) + row * a.xs + c0;
     const T *z = MODE == 1 || MODE == 2 ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr;
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(256) norm_fwd_kernel(Args a)
 #pragma unroll
         for (int i = 0; i < V; ++i) ss = fmaf(v[k][i], v[k][i], ss);
     }
-    const float rstd = 1.0f / sqrtf(team_sum<TEAM>(ss, sm) / (float)gs + a.eps);
+    const float rstd = 1.0f / sqrtf(team_sum<WARP>(make_float2(ss, 0.0f), sm, 0).x / (float)gs + a.eps);
     T *y = static_cast<T *>(a.y) + row * a.D + c0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -166,115 +175,125 @@ __global__ void __launch_bounds__(256) norm_fwd_kernel(Args a)
     }
 }
 
+// A vector's worth of one tensor as loaded: V elements of E.
+template <typename E, int V>
+struct Raw {
+    uint4 q[V * sizeof(E) / 16];
+    __device__ __forceinline__ void load(const E *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)(V * sizeof(E) / 16); ++i) q[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        return to_f32(reinterpret_cast<const E *>(q)[i]);
+    }
+};
+
 // Teams walk rows with a stride; thread l keeps the weight-gradient sums of its columns.
-template <typename T, typename R, int MODE, int TEAM, int K>
-__global__ void __launch_bounds__(256) norm_bwd_kernel(Args a)
+template <typename T, typename R, int MODE, bool WARP, int K, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
 {
     constexpr int V = VecOf<T>::v;
-    __shared__ float sm[8];
-    const int l = threadIdx.x % TEAM;
-    const int64_t team = (int64_t)blockIdx.x * (256 / TEAM) + threadIdx.x / TEAM;
-    const int64_t teams = (int64_t)gridDim.x * (256 / TEAM);
+    __shared__ float2 sm[2][32];
+    const int TEAM = WARP ? 32 : blockDim.x;
+    const int l = WARP ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t team = WARP ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
+    const int64_t teams = (int64_t)gridDim.x * (WARP ? 8 : 1);
     const int gs = a.group, c0 = blockIdx.y * gs;
-    float dw[K][V] = {}, ds[MODE == 3 ? K : 1][V] = {};
-    for (int64_t row = team; row < a.tok; row += teams) {
-        const T *x = a.x ? static_cast<const T *>(a.x) + row * a.xs + c0 : nullptr;
-        const T *z = MODE == 1 || MODE == 2 ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr;
-        const T *dyp = static_cast<const T *>(a.dy) + row * a.D + c0;
-        const R *xr = MODE == 3 ? static_cast<const R *>(a.xres) + row * a.D : nullptr;
-        // v: the normed value; q: dy (times the gate for MODE 2)
-        float v[K][V], q[K][V], ss = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (l + TEAM * k) * V;
-            if (c >= gs) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[k][i] = q[k][i] = 0.0f;
-                continue;
-            }
-            if (MODE == 3) load_f<R, V>(xr + c, v[k]);
-            else load_f<T, V>(x + c, v[k]);
-            load_f<T, V>(dyp + c, q[k]);
-            float wv[V];
-            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
-            if (MODE == 1 || MODE == 2) {
-                float zv[V];
-                load_f<T, V>(z + c, zv);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float gv = zv[i] * sigmoid_of(zv[i], T());
-                    if (MODE == 1) v[k][i] *= gv;
-                    else q[k][i] *= gv;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                ss = fmaf(v[k][i], v[k][i], ss);
-                dot = fmaf(a.w ? q[k][i] * wv[i] : q[k][i], v[k][i], dot);
-            }
-        }
-        ss = team_sum<TEAM>(ss, sm);
-        dot = team_sum<TEAM>(dot, sm);
-        const float rstd = 1.0f / sqrtf(ss / (float)gs + a.eps);
-        const float m = dot * rstd * rstd / (float)gs;  // mean(dh vh) rstd, for vh = v rstd
+    struct Row {
+        Raw<T, V> x, dy;                     // x of MODE 3 only for its scale's gradient
+        Raw<T, MODE == 1 || MODE == 2 ? V : 16 / sizeof(T)> z;
+        Raw<R, V> r, g;                      // MODE 3: the stream and its incoming gradient
+    };
+    Row cur[K];
+    auto load = [&](int64_t row, Row (&to)[K]) {
+        if (row >= a.tok) return;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (l + TEAM * k) * V;
             if (c >= gs) continue;
-            float wv[V], out[V];
-            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
-            else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) wv[i] = 1.0f;
+            const int64_t at = row * a.D + c0 + c;
+            to[k].dy.load(static_cast<const T *>(a.dy) + at);
+            if (MODE != 3 || a.has_ds) to[k].x.load(static_cast<const T *>(a.x) + row * a.xs + c0 + c);
+            if (MODE == 1 || MODE == 2) to[k].z.load(static_cast<const T *>(a.z) + row * a.zs + c0 + c);
+            if (MODE == 3) {
+                to[k].r.load(static_cast<const R *>(a.xres) + at);
+                if (a.dro) to[k].g.load(static_cast<const R *>(a.dro) + at);
             }
+        }
+    };
+    float dw[K][V] = {}, ds[MODE == 3 ? K : 1][V] = {};
+    load(team, cur);
+    int turn = 0;
+    for (int64_t row = team; row < a.tok; row += teams, ++turn) {
+        Row next[K];
+        load(row + teams, next);
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (l + TEAM * k) * V;
+            if (c >= gs) continue;
+            float wv[V];
+            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                dw[k][i] = fmaf(q[k][i], v[k][i] * rstd, dw[k][i]);
-                out[i] = rstd * (q[k][i] * wv[i] - v[k][i] * m);  // dv
+                float v = MODE == 3 ? cur[k].r[i] : cur[k].x[i], q = cur[k].dy[i];
+                if (MODE == 1 || MODE == 2) {
+                    const float zv = cur[k].z[i], gv = zv * sigmoid_of(zv, T());
+                    if (MODE == 1) v *= gv;
+                    else q *= gv;
+                }
+                ss = fmaf(v, v, ss);
+                dot = fmaf(a.w ? q * wv[i] : q, v, dot);
             }
-            if (MODE == 0) {
-                store_f<T, V>(static_cast<T *>(a.dx) + row * a.D + c0 + c, out);
-            } else if (MODE == 3) {
-                float sc[V], o2[V];
-                if (a.dro) {
-                    load_rw<R, V>(static_cast<const R *>(a.dro) + row * a.D + c, o2);
+        }
+        const float2 both = team_sum<WARP>(make_float2(ss, dot), sm, turn);
+        const float rstd = 1.0f / sqrtf(both.x / (float)gs + a.eps);
+        const float m = both.y * rstd * rstd / (float)gs;  // mean(dh vh) rstd, for vh = v rstd
 #pragma unroll
-                    for (int i = 0; i < V; ++i) out[i] += o2[i];
-                }
-                if (a.dres) store_f<R, V>(static_cast<R *>(a.dres) + row * a.D + c, out);
-                if (a.scale) load_f<float, V>(a.scale + c, sc);
-                if (a.has_ds) {
-                    float xv[V];
-                    load_f<T, V>(x + c, xv);
+        for (int k = 0; k < K; ++k) {
+            const int c = (l + TEAM * k) * V;
+            if (c >= gs) continue;
+            const int64_t at = row * a.D + c0 + c;
+            float wv[V], o1[V], o2[V];
+            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) ds[k][i] = fmaf(a.alpha * out[i], xv[i], ds[k][i]);
+            for (int i = 0; i < V; ++i) {
+                const float w = a.w ? wv[i] : 1.0f, yv = cur[k].dy[i];
+                if (MODE == 0) {
+                    const float v = cur[k].x[i];
+                    dw[k][i] = fmaf(yv, v * rstd, dw[k][i]);
+                    o1[i] = rstd * (yv * w - v * m);
+                } else if (MODE == 3) {
+                    const float v = cur[k].r[i];
+                    dw[k][i] = fmaf(yv, v * rstd, dw[k][i]);
+                    o1[i] = rstd * (yv * w - v * m) + (a.dro ? cur[k].g[i] : 0.0f);
+                    if (a.has_ds) ds[k][i] = fmaf(a.alpha * o1[i], cur[k].x[i], ds[k][i]);
+                } else {
+                    const float xv = cur[k].x[i], zv = cur[k].z[i], sg = sigmoid_of(zv, T());
+                    const float gv = zv * sg, dsilu = sg * fmaf(zv, 1.0f - sg, 1.0f);
+                    const float v = MODE == 1 ? xv * gv : xv, q = MODE == 1 ? yv : yv * gv;
+                    dw[k][i] = fmaf(q, v * rstd, dw[k][i]);
+                    const float dv = rstd * (q * w - v * m);
+                    o1[i] = MODE == 1 ? dv * gv : dv;
+                    o2[i] = (MODE == 1 ? dv * xv : yv * (xv * rstd) * w) * dsilu;
                 }
+            }
+            if (MODE == 3) {
+                if (a.dres) store_f<R, V>(static_cast<R *>(a.dres) + at, o1);
                 if (a.dx) {
+                    float sc[V];
+                    if (a.scale) load_f<float, V>(a.scale + c, sc);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o2[i] = out[i] * (a.scale ? a.alpha * sc[i] : a.alpha);
-                    store_f<T, V>(static_cast<T *>(a.dx) + row * a.D + c, o2);
+                    for (int i = 0; i < V; ++i) o2[i] = o1[i] * (a.scale ? a.alpha * sc[i] : a.alpha);
+                    store_f<T, V>(static_cast<T *>(a.dx) + at, o2);
                 }
             } else {
-                // x and z again, from cache: keeping them would cost 2 K V registers
-                float xv[V], zv[V], yv[V], dxv[V], dzv[V];
-                load_f<T, V>(x + c, xv);
-                load_f<T, V>(z + c, zv);
-                if (MODE == 2) load_f<T, V>(dyp + c, yv);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float sg = sigmoid_of(zv[i], T());
-                    const float dsilu = sg * fmaf(zv[i], 1.0f - sg, 1.0f);
-                    if (MODE == 1) {
-                        dxv[i] = out[i] * (zv[i] * sg);
-                        dzv[i] = out[i] * xv[i] * dsilu;
-                    } else {
-                        dxv[i] = out[i];
-                        dzv[i] = yv[i] * (xv[i] * rstd) * wv[i] * dsilu;
-                    }
-                }
-                store_f<T, V>(static_cast<T *>(a.dx) + row * a.D + c0 + c, dxv);
-                if (a.dz) store_f<T, V>(static_cast<T *>(a.dz) + row * a.D + c0 + c, dzv);
+                store_f<T, V>(static_cast<T *>(a.dx) + at, o1);
+                if (MODE != 0 && a.dz) store_f<T, V>(static_cast<T *>(a.dz) + at, o2);
             }
+            cur[k] = next[k];
         }
     }
 #pragma unroll
@@ -308,7 +327,7 @@ __device__ __forceinline__ float normed(const Args &a, int64_t row, int c0, int 
 template <typename T, typename R, int MODE>
 __global__ void __launch_bounds__(256) norm_fwd_any_kernel(Args a)
 {
-    __shared__ float sm[8];
+    __shared__ float2 sm[2][32];
     const int64_t row = blockIdx.x;
     const int gs = a.group, c0 = blockIdx.y * gs;
     const T *x = static_cast<const T *>(a.x) + row * a.xs + c0;
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(256) norm_fwd_any_kernel(Args a)
         }
         ss = fmaf(v, v, ss);
     }
-    const float rstd = 1.0f / sqrtf(team_sum<256>(ss, sm) / (float)gs + a.eps);
+    const float rstd = 1.0f / sqrtf(team_sum<false>(make_float2(ss, 0.0f), sm, 0).x / (float)gs + a.eps);
     for (int c = threadIdx.x; c < gs; c += 256) {
         gate = 1.0f;
         float v = MODE == 3 ? stream(c) : normed<T, R, MODE>(a, row, c0, c, gate);
@@ -349,7 +368,7 @@ __global__ void __launch_bounds__(256) norm_fwd_any_kernel(Args a)
 template <typename T, typename R, int MODE>
 __global__ void __launch_bounds__(256) norm_bwd_any_kernel(Args a)
 {
-    __shared__ float sm[8];
+    __shared__ float2 sm[2][32];
     const int gs = a.group, c0 = blockIdx.y * gs;
     const int64_t team = blockIdx.x, teams = gridDim.x;
     float *pw = a.part + team * a.D + c0, *ps = a.part + (teams + team) * a.D + c0;
@@ -357,7 +376,8 @@ __global__ void __launch_bounds__(256) norm_bwd_any_kernel(Args a)
         if (a.has_dw) pw[c] = 0.0f;
         if (a.has_ds) ps[c] = 0.0f;
     }
-    for (int64_t row = team; row < a.tok; row += teams) {
+    int turn = 0;
+    for (int64_t row = team; row < a.tok; row += teams, ++turn) {
         const T *dyp = static_cast<const T *>(a.dy) + row * a.D + c0;
         float ss = 0.0f, dot = 0.0f, gate;
         for (int c = threadIdx.x; c < gs; c += 256) {
@@ -367,10 +387,9 @@ __global__ void __launch_bounds__(256) norm_bwd_any_kernel(Args a)
             ss = fmaf(v, v, ss);
             dot = fmaf(q, v, dot);
         }
-        ss = team_sum<256>(ss, sm);
-        dot = team_sum<256>(dot, sm);
-        const float rstd = 1.0f / sqrtf(ss / (float)gs + a.eps);
-        const float m = dot * rstd * rstd / (float)gs;
+        const float2 both = team_sum<false>(make_float2(ss, dot), sm, turn);
+        const float rstd = 1.0f / sqrtf(both.x / (float)gs + a.eps);
+        const float m = both.y * rstd * rstd / (float)gs;
         for (int c = threadIdx.x; c < gs; c += 256) {
             const float v = normed<T, R, MODE>(a, row, c0, c, gate);
             const float w = a.w ? a.w[c0 + c] : 1.0f, dyv = to_f32(dyp[c]);
@@ -401,23 +420,28 @@ __global__ void __launch_bounds__(256) norm_bwd_any_kernel(Args a)
     }
 }
 
-// out[c] = sum over partial rows, in a fixed order: 32 columns by 8 strides of rows per block.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float *part, int parts, int D, float *out)
+// out[c] = sum over partial rows, in a fixed order: 32 columns by 32 strides of rows a block.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *part, int parts, int D, float *out)
 {
-    __shared__ double sm[8][32];
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, r0 = threadIdx.x / 32;
+    __shared__ double sm[32][32];
+    const int lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane, r0 = threadIdx.x / 32;
     double s = 0.0;
     if (c < D)
-        for (int r = r0; r < parts; r += 8) s += part[(int64_t)r * D + c];
-    sm[r0][threadIdx.x % 32] = s;
+#pragma unroll 4
+        for (int r = r0; r < parts; r += 32) s += part[(int64_t)r * D + c];
+    sm[r0][lane] = s;
     __syncthreads();
     if (r0 == 0 && c < D) {
-        for (int i = 1; i < 8; ++i) s += sm[i][threadIdx.x];
+#pragma unroll 8
+        for (int i = 1; i < 32; ++i) s += sm[i][lane];
         out[c] = (float)s;
     }
 }
 
 bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Threads of a block that has K vectors of a row in each.
+unsigned block_of(int nv, int K) { return (unsigned)(((nv + K - 1) / K + 31) / 32 * 32); }
 
 template <typename T, typename R, int MODE>
 cudaError_t fwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st)
@@ -427,34 +451,56 @@ cudaError_t fwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st)
     const int nv = (int)(n.group / V);
     const dim3 warps((unsigned)((n.tok + 7) / 8), groups), rows((unsigned)n.tok, groups);
     if (!vec || nv > 2048) norm_fwd_any_kernel<T, R, MODE><<<rows, 256, 0, st>>>(a);
-    else if (nv <= 32) norm_fwd_kernel<T, R, MODE, 32, 1><<<warps, 256, 0, st>>>(a);
-    else if (nv <= 64) norm_fwd_kernel<T, R, MODE, 32, 2><<<warps, 256, 0, st>>>(a);
-    else if (nv <= 256) norm_fwd_kernel<T, R, MODE, 256, 1><<<rows, 256, 0, st>>>(a);
-    else if (nv <= 512) norm_fwd_kernel<T, R, MODE, 256, 2><<<rows, 256, 0, st>>>(a);
-    else if (nv <= 1024) norm_fwd_kernel<T, R, MODE, 256, 4><<<rows, 256, 0, st>>>(a);
-    else norm_fwd_kernel<T, R, MODE, 256, 8><<<rows, 256, 0, st>>>(a);
+    else if (nv <= 32) norm_fwd_kernel<T, R, MODE, true, 1><<<warps, 256, 0, st>>>(a);
+    else if (nv <= 64) norm_fwd_kernel<T, R, MODE, true, 2><<<warps, 256, 0, st>>>(a);
+    else if (nv <= 256) norm_fwd_kernel<T, R, MODE, false, 1><<<rows, block_of(nv, 1), 0, st>>>(a);
+    else if (nv <= 1024) norm_fwd_kernel<T, R, MODE, false, 2><<<rows, block_of(nv, 2), 0, st>>>(a);
+    else norm_fwd_kernel<T, R, MODE, false, 4><<<rows, block_of(nv, 4), 0, st>>>(a);
     return cudaGetLastError();
+}
+
+// Blocks of a kernel that fit the GPU at once: a backward block walks rows until none is
+// left, so one more wave of blocks would run almost alone.
+int resident(const void *kernel, int threads)
+{
+    int dev = 0, sms = 148, per = 1;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) != cudaSuccess || per < 1) per = 1;
+    return per * sms;
 }
 
 template <typename T, typename R, int MODE>
 cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int *parts)
 {
     constexpr int V = VecOf<T>::v;
-    const unsigned groups = (unsigned)(n.D / n.group);
+    const int64_t groups = n.D / n.group;
     const int nv = (int)(n.group / V);
-    const bool team32 = vec && nv <= 64;
-    // enough blocks to fill the GPU over all groups, few enough partial rows
-    int64_t blocks = team32 ? (n.tok + 7) / 8 : n.tok;
-    const int64_t most = team32 ? kParts / 8 : kParts / 2;
+    const bool warp = vec && nv <= 64;
+    void (*kernel)(Args);
+    int threads = 256;
+    if (!vec || nv > 1024) {
+        kernel = norm_bwd_any_kernel<T, R, MODE>;
+    } else if (nv <= 32) {
+        kernel = norm_bwd_kernel<T, R, MODE, true, 1, 256, 2>;
+    } else if (nv <= 64) {
+        kernel = norm_bwd_kernel<T, R, MODE, true, 2, 256, 2>;
+    } else if (nv <= 320) {
+        kernel = norm_bwd_kernel<T, R, MODE, false, 1, 320, 3>;
+        threads = (int)block_of(nv, 1);
+    } else if (nv <= 640) {
+        kernel = norm_bwd_kernel<T, R, MODE, false, 2, 320, 2>;
+        threads = (int)block_of(nv, 2);
+    } else {
+        kernel = norm_bwd_kernel<T, R, MODE, false, 2, 512, 1>;
+        threads = (int)block_of(nv, 2);
+    }
+    // one wave of blocks over all groups, and no more partial rows than the workspace has
+    int64_t blocks = warp ? (n.tok + 7) / 8 : n.tok, most = resident((const void *)kernel, threads) / groups;
+    if (most > kParts / (warp ? 8 : 1)) most = kParts / (warp ? 8 : 1);
+    if (most < 1) most = 1;
     if (blocks > most) blocks = most;
-    const dim3 grid((unsigned)blocks, groups);
-    *parts = (int)(team32 ? blocks * 8 : blocks);
-    if (!vec || nv > 1024) norm_bwd_any_kernel<T, R, MODE><<<grid, 256, 0, st>>>(a);
-    else if (nv <= 32) norm_bwd_kernel<T, R, MODE, 32, 1><<<grid, 256, 0, st>>>(a);
-    else if (nv <= 64) norm_bwd_kernel<T, R, MODE, 32, 2><<<grid, 256, 0, st>>>(a);
-    else if (nv <= 256) norm_bwd_kernel<T, R, MODE, 256, 1><<<grid, 256, 0, st>>>(a);
-    else if (nv <= 512) norm_bwd_kernel<T, R, MODE, 256, 2><<<grid, 256, 0, st>>>(a);
-    else norm_bwd_kernel<T, R, MODE, 256, 4><<<grid, 256, 0, st>>>(a);
+    *parts = (int)(warp ? blocks * 8 : blocks);
+    kernel<<<dim3((unsigned)blocks, (unsigned)groups), threads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -538,7 +584,7 @@ cudaError_t launch_norm_bwd(const NormArgs &n, cudaStream_t st, int *launches)
     float *outs[2] = {n.dweight, n.dscale};
     for (int i = 0; i < 2; ++i) {
         if (!outs[i]) continue;
-        norm_reduce_kernel<<<blocks, 256, 0, st>>>(n.partials + (size_t)i * parts * n.D, parts,
+        norm_reduce_kernel<<<blocks, 1024, 0, st>>>(n.partials + (size_t)i * parts * n.D, parts,
                                                    (int)n.D, outs[i]);
         ++*launches;
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
