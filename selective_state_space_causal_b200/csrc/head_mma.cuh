@@ -137,7 +137,7 @@ constexpr int64_t kMark = (int64_t)64 * NPAD;  // elements of one plane
 
 // Scratch that one call needs, carved from the workspace in this order.
 struct Layout {
-    size_t tab, seg, segdec, marks, total;
+    size_t tab, seg, segdec, marks, order, total;
 };
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -155,7 +155,9 @@ struct StateArgs {
     int64_t span;       // tokens of a segment (a multiple of kC)
     float *seg;         // split walks: (segment slot, panel, NPAD / 4, 64, 4) end, then start states
     float *segdec;      // (segment slot, head): the segment's decay
-    int segment;        // 0: whole sequences; 1, 2: the passes of a split walk
+    int32_t *order;     // room for the sequences' order, or nullptr
+    int segment = 0;    // 0: whole sequences; 1, 2: the passes of a split walk
+    int width = 2;      // panels of a CTA
 };
 
 // Steps and running decays of every chunk.

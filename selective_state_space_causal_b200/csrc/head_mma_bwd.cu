@@ -41,7 +41,7 @@ struct BwdArgs {
 
 constexpr int kWork = 16;  // compute warps
 constexpr int kBIssuer = kWork, kBLoader = kWork + 1, kBFinish = kWork + 2;
-constexpr int kBwdThreads = (kWork + 3) * 32;
+constexpr int kFinish = 2, kBwdThreads = (kBFinish + kFinish) * 32;
 
 // Sums over a panel that one warp finishes; two buffers.
 struct Sums {
@@ -254,52 +254,53 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             }
         }
         __syncwarp();
-    } else if (warp == kBFinish) {
-        // tokens 4 lane .. 4 lane + 3; sums over a head's panels, then the head's gradients
+    } else if (warp >= kBFinish) {
+        // two warps, heads in turn: tokens 4 lane .. 4 lane + 3, sums over a head's panels,
+        // then the head's gradients
         float R[4], K[4], I[4], J[4], own[4], dsk = 0.0f, dot = 0.0f;
+        auto add4 = [&](float (&v)[4], const float *q) {
+            const float4 x = *reinterpret_cast<const float4 *>(q + 4 * lane);
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        };
         for (int it = 0; it < count; ++it) {
+            if (it / z.np % kFinish != warp - kBFinish) continue;
             const PanelRef p = panel_of(z, g, pb + it);
             const bool start = p.p0 == 0, end = p.p0 + 64 >= z.P;
             const float *tb = a.tab + (slot * z.H + p.h) * kTab;
+            // what the end needs from memory is on its way during the wait
+            const float bias = a.dt_bias ? a.dt_bias[p.h] : 0.0f, Ah = a.A[p.h], last = tb[kTabEc + kC - 1];
+            const float4 d4 = *reinterpret_cast<const float4 *>(tb + kTabD + 4 * lane);
+            const float4 e4 = *reinterpret_cast<const float4 *>(tb + kTabEc + 4 * lane);
+            const float4 w4 = *reinterpret_cast<const float4 *>(tb + kTabWn + 4 * lane);
             float raw4[4];
-            if (end) {
-                const float bias = a.dt_bias ? a.dt_bias[p.h] : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 4 * lane + e;
-                    raw4[e] = t < len ? to_f32(a.delta[(ck.start + t) * a.delta_stride + p.h]) + bias : 0.0f;
-                }
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * lane + e;
+                raw4[e] = t < len ? to_f32(a.delta[(ck.start + t) * a.delta_stride + p.h]) + bias : 0.0f;
             }
-            wait(&epi[it & 1], it >> 1);
-            const Sums &s = sums[it & 1];
             if (start) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) R[e] = K[e] = I[e] = J[e] = own[e] = 0.0f;
                 dsk = dot = 0.0f;
             }
+            wait(&epi[it & 1], it >> 1);
+            const Sums &s = sums[it & 1];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 4 * lane + e;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (32 * q <= t) R[e] += s.r[q][t];  // later blocks hold no row before t
-                    K[e] += s.k[q][t];
-                    I[e] += s.i[q][t];
-                    J[e] += s.j[q][t];
-                }
-                own[e] += s.own[t];
+            for (int q = 0; q < 4; ++q) {
+                if (q <= lane / 8) add4(R, s.r[q]);  // later blocks hold no row before these tokens
+                add4(K, s.k[q]);
+                add4(I, s.i[q]);
+                add4(J, s.j[q]);
             }
+            add4(own, s.own);
             dsk += lane < kWork ? s.skip[lane] : 0.0f;
             dot += lane < kWork ? s.dot[lane] : 0.0f;
             __syncwarp();
             if (lane == 0) mbar_arrive(&fin[it & 1]);
             if (!end) continue;
-            const float4 d4 = *reinterpret_cast<const float4 *>(tb + kTabD + 4 * lane);
-            const float4 e4 = *reinterpret_cast<const float4 *>(tb + kTabEc + 4 * lane);
-            const float4 w4 = *reinterpret_cast<const float4 *>(tb + kTabWn + 4 * lane);
             const float d[4] = {d4.x, d4.y, d4.z, d4.w}, ec[4] = {e4.x, e4.y, e4.z, e4.w};
             const float wn[4] = {w4.x, w4.y, w4.z, w4.w};
-            const float X = warp_sum(dot) * tb[kTabEc + kC - 1];
+            const float X = warp_sum(dot) * last;
             // gradient of log a_r from what passes through token r: outputs at or after it
             // from inputs before it (a suffix sum of rows less columns, the diagonal left
             // out since it would cancel only up to rounding), from the start state, and the
@@ -325,7 +326,6 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             }
             ta -= sa;
             tp -= sb;
-            const float Ah = a.A[p.h];
             float pa = 0.0f, pbias = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             const float ds = tb[kTabD + row], ls = tb[kTabL + row];
             wait(&dm, it);
             umma::fence_after();
-            float ks = 0.0f;
+            float own = 0.0f;
             const f32x2 d2 = pk2(ds, ds);
             f32x2 k2 = pk2(0.0f, 0.0f);
 #pragma unroll
@@ -440,9 +440,9 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
                     f32x2 wl = mul2(m2, gl);
                     if (j == wi) {  // the diagonal apart
                         upk2(wl, w0, w1);
-                        if (8 * cg + c == lane) { s.own[row] = w0; w0 = 0.0f; }
-                        if (8 * cg + c + 1 == lane) { s.own[row] = w1; w1 = 0.0f; }
-                        wl = pk2(w0, w1);
+                        const bool q0 = 8 * cg + c == lane, q1 = 8 * cg + c + 1 == lane;
+                        own = q0 ? w0 : q1 ? w1 : own;
+                        wl = pk2(q0 ? 0.0f : w0, q1 ? 0.0f : w1);
                     }
                     k2 = add2(k2, wl);
                     upk2(mul2(wl, d2), wd[c], wd[c + 1]);
@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             if (lane == 0) mbar_arrive(&mt);
             float k0, k1;
             upk2(k2, k0, k1);
-            ks = k0 + k1;
-            s.k[cg][row] = ks;
+            s.k[cg][row] = k0 + k1;
+            if (lane / 8 == cg) s.own[row] = own;
 
             // columns 16 cg .. of the panel: du of row s, and the dots of rows s and t
             const float wf = tb[kTabWf + row];
@@ -801,7 +801,7 @@ BwdLayout bwd_layout(const Dims &z)
     l.span = segment_span(z, &l.split);
     l.walk = layout_of(z, 2, l.span, l.split);
     const int64_t slots = head_slots(z.tok, z.S, kC);
-    const size_t marks = l.walk.total - l.walk.marks;
+    const size_t marks = l.walk.order - l.walk.marks;
     // whole heads per CTA; G^T and the rounded dG^T are shared by a CTA's panels, so as few
     // ranges as leave about three CTAs an SM
     int64_t heads = z.H / z.G, per = slots * z.G * heads / (148 * 3);
@@ -827,6 +827,7 @@ cudaError_t launch_backward(const HeadScanArgs &a, cudaStream_t st, int *launche
     float *tab = reinterpret_cast<float *>(ws + l.walk.tab);
     bf16 *S0 = reinterpret_cast<bf16 *>(ws + l.walk.marks), *dS = reinterpret_cast<bf16 *>(ws + l.dS);
     float *seg = reinterpret_cast<float *>(ws + l.walk.seg), *segdec = reinterpret_cast<float *>(ws + l.walk.segdec);
+    int32_t *order = a.cu && a.S > 1 ? reinterpret_cast<int32_t *>(ws + l.walk.order) : nullptr;
     float *part = reinterpret_cast<float *>(ws + l.part);
     if (cudaError_t e = launch_tables(a, z, tab, true, st, launches); e != cudaSuccess) return e;
     const int64_t row = a.H * a.P;
@@ -834,9 +835,9 @@ cudaError_t launch_backward(const HeadScanArgs &a, cudaStream_t st, int *launche
     const bool vec = bc_vec && vec16(a.u, a.u_stride, a.P) && vec16(a.dy, row, a.P);
     const bf16 *u = static_cast<const bf16 *>(a.u), *dy = static_cast<const bf16 *>(a.dy);
     const bf16 *B = static_cast<const bf16 *>(a.B), *C = static_cast<const bf16 *>(a.C);
-    StateArgs s{z, u, a.u_stride, B, a.bc_stride, tab, a.h0, nullptr, S0, l.span, seg, segdec, 0};
+    StateArgs s{z, u, a.u_stride, B, a.bc_stride, tab, a.h0, nullptr, S0, l.span, seg, segdec, order};
     if (cudaError_t e = launch_states(s, false, 2, l.split, vec, st, launches); e != cudaSuccess) return e;
-    StateArgs r{z, dy, row, C, a.bc_stride, tab, a.dh_final, a.dh0, dS, l.span, seg, segdec, 0};
+    StateArgs r{z, dy, row, C, a.bc_stride, tab, a.dh_final, a.dh0, dS, l.span, seg, segdec, order};
     if (cudaError_t e = launch_states(r, true, 2, l.split, vec, st, launches); e != cudaSuccess) return e;
     const int64_t slots = head_slots(z.tok, z.S, kC);
     BwdArgs b{z, u, dy, B, C, static_cast<const bf16 *>(a.delta), a.u_stride, a.bc_stride, a.delta_stride,

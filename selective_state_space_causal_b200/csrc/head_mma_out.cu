@@ -332,7 +332,8 @@ cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t st, int *launches
     const bool vec = vec16(a.B, a.bc_stride, a.N) && vec16(a.C, a.bc_stride, a.N) && vec16(a.u, a.u_stride, a.P);
     StateArgs s{z, static_cast<const bf16 *>(a.u), a.u_stride, static_cast<const bf16 *>(a.B), a.bc_stride,
                 tab, a.h0, a.h_final, marks, span, reinterpret_cast<float *>(ws + l.seg),
-                reinterpret_cast<float *>(ws + l.segdec), 0};
+                reinterpret_cast<float *>(ws + l.segdec),
+                a.cu && a.S > 1 ? reinterpret_cast<int32_t *>(ws + l.order) : nullptr};
     if (cudaError_t e = launch_states(s, false, 1, split, vec, st, launches); e != cudaSuccess) return e;
     if (a.tok == 0) return cudaSuccess;
     const int64_t slots = head_slots(z.tok, z.S, kC);

@@ -13,6 +13,9 @@
 #include "head_mma.cuh"
 
 namespace ssm {
+
+cudaError_t launch_seq_order(const int32_t *cu, int64_t S, int64_t tok, int32_t *order, cudaStream_t stream);
+
 namespace hm {
 
 __device__ int g_status;
@@ -129,7 +132,7 @@ constexpr int state_smem()
     return 1024 + kStages * state_stage<NPAD>();
 }
 
-// One CTA has two panels of one group and walks a segment's chunks. The warps have
+// One CTA has one or two panels of one group and walks a segment's chunks. The warps have
 // roles, so that loads, conversion, matrix instructions and state updates of
 // neighbouring chunks run at the same time (with all warps in step, each phase's
 // latency was exposed: 5500 clocks a chunk against 1536 of matrix instructions):
@@ -154,8 +157,11 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     __shared__ uint32_t tmem_slot;
     const Dims &z = a.z;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int64_t slot = blockIdx.x;
-    const int pairs = (z.npan + 1) / 2, g = blockIdx.y / pairs, pair = blockIdx.y % pairs;
+    // whole sequences go longest first: a long one started last would run almost alone
+    const int64_t slot = a.order ? a.order[blockIdx.y] : blockIdx.y;
+    const int per_group = (z.npan + a.width - 1) / a.width;
+    const int g = blockIdx.x / per_group, pan0 = blockIdx.x % per_group * a.width;
+    const int np = min(a.width, z.npan - pan0);  // panels of this CTA
     const ChunkRef sg = find_chunk(z.cu, z.S, z.tok, a.span, slot);
     if (sg.len == 0 && (sg.k != 0 || a.segment != 0)) return;
     const int nchunk = (sg.len + kC - 1) / kC;
@@ -190,8 +196,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, failed, &g_status); };
 
     if (warp == kLoader) {
-        const int np = min(2, z.npan - 2 * pair);  // panels there are
-        const PanelRef q0 = panel_of(z, g, 2 * pair), q1 = panel_of(z, g, 2 * pair + np - 1);
+        const PanelRef q0 = panel_of(z, g, pan0), q1 = panel_of(z, g, pan0 + np - 1);
         for (int kk = 0; kk < nchunk; ++kk) {
             const int k = chunk_at(kk), sg_i = kk % kStages;
             const int64_t t0 = sg.start + (int64_t)k * kC;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     } else if (warp < kConvWarps) {
         // 32 tokens at a time; this warp has state rows 32 (warp % 4) .. of the two panels
         const int grp = warp / 4, w4 = warp % 4, cp = w4 / 2;
-        const bool has_x = 2 * pair + cp < z.npan;
+        const bool has_x = cp < np;  // without a second panel its half of the product is never read
         const uint32_t rows = (uint32_t)w4 << 21;
         // the tiles of ldsm_t: tokens 0-7, rows 0-7; the same tokens, rows 8-15; tokens 8-15
         const int tt = lane % 8 + (lane / 16) * 8, pc = (w4 & 1) * 4 + (lane / 8) % 2;
@@ -287,18 +292,18 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
                 fence_proxy_async();
             }
 #pragma unroll
-            for (int ph = 0; ph < 2; ++ph) {  // 16 state rows
+            for (int ph = 0; ph < 2 && has_x; ++ph) {  // 16 state rows
                 uint32_t x[8], v[3][8];
 #pragma unroll
                 for (int th = 0; th < 2; ++th)  // 16 tokens
                     umma::ldsm_t(sx + cp * umma::kPanel + umma::piece(32 * q + 16 * th + tt, pc + 2 * ph),
                                  x[4 * th], x[4 * th + 1], x[4 * th + 2], x[4 * th + 3]);
-                if (len < 32 || !has_x) {
+                if (len < 32) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int t = 8 * (i / 2) + 2 * (lane % 4);
                         const uint32_t keep = (t < len ? 0xFFFFu : 0u) | (t + 1 < len ? 0xFFFF0000u : 0u);
-                        x[i] &= has_x ? keep : 0u;
+                        x[i] &= keep;
                     }
                 }
 #pragma unroll
@@ -318,8 +323,8 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     } else {
         // row sr of the two panels, columns n0 ..
         const int sw = warp - kConvWarps, sr = (sw & 3) * 32 + lane, n0 = (sw / 4) * COLS;
-        const int si = 2 * pair + sr / 64, p = sr % 64;
-        const bool has_s = si < z.npan;
+        const int si = pan0 + sr / 64, p = sr % 64;
+        const bool has_s = sr / 64 < np;
         const PanelRef sp = panel_of(z, g, min(si, z.npan - 1));
         const bool row_in = has_s && p < sp.rows;
         const int64_t dir = REV ? -1 : 1, c0 = first + chunk_at(0);
@@ -380,7 +385,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
             wait(&summed[kk & 1], kk >> 1);
             umma::fence_after();
 #pragma unroll
-            for (int j = 0; j < COLS / 16; ++j) {
+            for (int j = 0; j < COLS / 16 && has_s; ++j) {
                 uint32_t v[16];
                 umma::ld16(umma::lanes(tm + (kk & 1) * NPAD + n0 + 16 * j, warp), v);
                 umma::wait_ld();
@@ -471,7 +476,8 @@ cudaError_t launch_walk(const StateArgs &a, cudaStream_t st, int *launches)
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e != cudaSuccess)
         return e;
-    const dim3 grid((unsigned)head_slots(a.z.tok, a.z.S, a.span), (unsigned)(a.z.G * ((a.z.npan + 1) / 2)));
+    const dim3 grid((unsigned)(a.z.G * ((a.z.npan + a.width - 1) / a.width)),
+                    (unsigned)head_slots(a.z.tok, a.z.S, a.span));
     CUtensorMap xmap{}, bmap{};
     if (VEC && a.z.tok > 0 &&
         (!umma::encode_3d(&xmap, a.x, a.z.tok, a.z.H, a.z.P, a.x_stride) ||
@@ -490,6 +496,14 @@ cudaError_t states(StateArgs a, bool split, bool vec, cudaStream_t st, int *laun
         return vec ? launch_walk<NPAD, REV, PLANES, true>(a, st, launches)
                    : launch_walk<NPAD, REV, PLANES, false>(a, st, launches);
     };
+    // one panel a CTA where two would leave SMs without one: a chunk then takes about 0.6 of
+    // the time, at the price of loading b twice
+    a.width = a.z.S * a.z.G * ((a.z.npan + 1) / 2) < 148 && !split ? 1 : 2;
+    if (split) a.order = nullptr;
+    else if (a.order) {
+        if (cudaError_t e = launch_seq_order(a.z.cu, a.z.S, a.z.tok, a.order, st); e != cudaSuccess) return e;
+        ++*launches;
+    }
     if (!split) return walk(0);
     if (cudaError_t e = walk(1); e != cudaSuccess) return e;
     head_join_kernel<NPAD, REV><<<dim3((unsigned)a.z.S, (unsigned)(a.z.G * a.z.npan)), 256, 0, st>>>(a);
@@ -562,7 +576,8 @@ Layout layout_of(const Dims &z, int planes, int64_t span, bool split)
     l.seg = l.tab + up256((size_t)slots * z.H * kTab * 4);
     l.segdec = l.seg + up256((size_t)segs * panel * 4);
     l.marks = l.segdec + up256((size_t)segs * z.H * 4);
-    l.total = l.marks + up256((size_t)slots * panel * 2 * planes);
+    l.order = l.marks + up256((size_t)slots * panel * 2 * planes);
+    l.total = l.order + up256(z.S > 1 ? (size_t)z.S * 4 : 0);
     return l;
 }
 
