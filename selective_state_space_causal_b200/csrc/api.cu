@@ -780,6 +780,15 @@ static int check_stride(const char *fn, const char *what, int64_t rows, int64_t 
                 what, (long long)stride, (long long)width);
 }
 
+// A single token has no next row: whatever strides came, the kernels see a row's width.
+static void lone_row(ssm::HeadScanArgs &a)
+{
+    if (a.tok > 1) return;
+    a.u_stride = a.H * a.P;
+    a.delta_stride = a.H;
+    a.bc_stride = a.G * a.N;
+}
+
 static bool head_ws_args_ok(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N, int64_t S,
                             ssm_dtype act_dtype)
 {
@@ -849,6 +858,7 @@ int ssm_head_scan_fwd(const void *u, int64_t u_stride, const void *delta, int64_
                         delta_softplus, h0, cu_seqlens, S, tok, H, P, G, N, dt(act_dtype),
                         workspace, y, h_final};
     if (int r = check_head_scan(fn, a, act_dtype)) return r;
+    lone_row(a);
     if (tok > 0 && !y) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: y is NULL", fn);
     const size_t need = ssm_head_scan_workspace_size(tok, H, P, G, N, S, act_dtype);
     if (int r = check_workspace(fn, workspace, workspace_bytes, need)) return r;
@@ -881,6 +891,7 @@ int ssm_head_scan_bwd(const void *u, int64_t u_stride, const void *delta, int64_
                         workspace, nullptr, nullptr, dy, dh_final, du, ddelta, dB, dC, dA, dDskip,
                         ddt_bias, dh0};
     if (int r = check_head_scan(fn, a, act_dtype)) return r;
+    lone_row(a);
     if (!dA) return fail(SSM_ERR_INVALID_ARGUMENT, "%s: dA is NULL", fn);
     if (tok > 0 && (!dy || !du || !ddelta || !dB || !dC))
         return fail(SSM_ERR_INVALID_ARGUMENT, "%s: dy, du, ddelta, dB and dC are required", fn);

@@ -11,7 +11,7 @@
 //   ec     2^{c_t}                  wf     d_t 2^{c_127 - c_t}
 //   col    2^{r_i - c_t} for blocks i = 1..3 and t < 32 i (192 values); times d_t in
 //          the forward's tables
-//   wn, el 2^{c_127 - c_t} and 2^{l_t}, for the backward
+//   wn, el 2^{c_127 - c_t} and 2^{l_t}, for the backward;  ll  what rounding l left
 #pragma once
 
 #include "head_scan.cuh"
@@ -48,8 +48,8 @@ __device__ __forceinline__ PanelRef panel_of(const Dims &z, int g, int pi)
 
 // Tables of one (chunk slot, head), in floats.
 constexpr int kTabD = 0, kTabL = kC, kTabEc = 2 * kC, kTabCol = 3 * kC, kTabWf = 3 * kC + 192;
-constexpr int kTabWn = kTabWf + kC, kTabEl = kTabWn + kC;
-constexpr int kTab = 6 * kC + 192;
+constexpr int kTabWn = kTabWf + kC, kTabEl = kTabWn + kC, kTabLl = kTabEl + kC;
+constexpr int kTab = 7 * kC + 192;
 constexpr int kTabOut = kTabWf;  // what the outputs need comes first
 __host__ __device__ constexpr int col_at(int i) { return kTabCol + (i == 1 ? 0 : i == 2 ? 32 : 96); }
 
@@ -157,7 +157,6 @@ struct StateArgs {
     float *segdec;      // (segment slot, head): the segment's decay
     int32_t *order;     // room for the sequences' order, or nullptr
     int segment = 0;    // 0: whole sequences; 1, 2: the passes of a split walk
-    int width = 2;      // panels of a CTA
 };
 
 // Steps and running decays of every chunk.
@@ -180,7 +179,9 @@ size_t forward_bytes(const Dims &z);
 
 inline bool vec16(const void *p, int64_t stride, int64_t width)
 {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0 && width % 8 == 0;
+    // a tile copy's strides end at 2^40 bytes
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0 && width % 8 == 0 &&
+           stride < ((int64_t)1 << 38);
 }
 
 }  // namespace hm

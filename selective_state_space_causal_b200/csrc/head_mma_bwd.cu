@@ -11,8 +11,9 @@
 //   dC = sum over panels of e^{c_t} dy S0 + dG B,   dB = the same of w_s u dS + dG^T C.
 //
 // What gradients of the decays are made of is never rounded to bf16: G and dM come from
-// the exact bf16 inputs, V and Yi from two planes of the states (16 bits), and the sums
-// are fp32. M and dG are rounded once, as left operands.
+// the exact bf16 inputs, V and Yi from two planes of the states (17 bits), and the sums
+// are fp32. Rounded to bf16 once: M as a left operand (of du), the states that dB and dC
+// take in from other chunks.
 #include <type_traits>
 
 #include "head_mma.cuh"
@@ -33,7 +34,7 @@ struct BwdArgs {
     const float *tab;
     const bf16 *S0, *dS;  // marks, two planes
     bf16 *du, *ddelta, *dB, *dC;
-    bf16 *dg;     // (slot, group, range) 128 x 128 tiles of dG^T as they lie in shared memory
+    bf16 *dg;     // (slot, group, range, 2 planes) 128 x 128 tiles of dG^T as they lie in shared memory
     float *part;  // (slot, head, 3)
     int per, ranges;  // panels of a CTA (whole heads), CTAs of a chunk and group
     bool du_vec;
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
     if (tid == 0) {
         mbar_init_n(&gbar, 1);
         mbar_init_n(&ss, 1);
-        mbar_init_n(&ss_free, kWork + 1);
+        mbar_init_n(&ss_free, kWork / 2 + 1);
         mbar_init_n(&dm, 1);
         mbar_init_n(&vy, 1);
         mbar_init_n(&mt, kWork);
@@ -355,13 +356,17 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
         {  // M^T is zero for t in blocks before s's, for every panel
             const uint32_t zero[4] = {};
             for (int j = 0; j < wi; ++j)
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
-                             :: "r"(kMt + me + 16 * j + 4 * cg), "r"(zero[0]), "r"(zero[1]), "r"(zero[2]), "r"(zero[3])
-                             : "memory");
+                umma::st4(kMt + me + 16 * j + 4 * cg, zero);
             umma::wait_st();
         }
         wait(&gbar, 0);
         umma::fence_after();
+        // A warp's lanes of tensor memory and its scheduler both go by warp % 4, and later
+        // rows have fewer columns t >= s: the warps of the last two blocks of rows take
+        // <S0, dS> as well, 5 of 8 pieces by the last's.
+        constexpr int DOTS = PLANE / 16;
+        const int dot0 = (wi == 3 ? 0 : DOTS * 5 / 8) + cg * 32 + lane, dot1 = wi == 3 ? DOTS * 5 / 8 : DOTS;
+        if (wi < 2 && lane == 0) sums[0].dot[warp] = sums[1].dot[warp] = 0.0f;
         float dg[4][8];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -373,29 +378,28 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             const float *tb = reinterpret_cast<const float *>(raw + (sT + (it & 1) * kTab * 4 - saddr(raw)));
             Sums &s = sums[it & 1];
             const float skip = a.Dskip ? a.Dskip[p.h] : 0.0f;
-            // <S0, dS> of this panel
-            wait(&ss, it);
             float dot = 0.0f;
+            if (wi >= 2) {  // <S0, dS> of this panel
+                wait(&ss, it);
+                for (int i = dot0; i < dot1; i += 128) {
+                    const uint32_t o = sS + i * 16;
+                    const uint4 ah = lds16(o), al = lds16(o + PLANE), bh = lds16(o + 2 * PLANE), bl = lds16(o + 3 * PLANE);
+                    const uint32_t A4[4] = {ah.x, ah.y, ah.z, ah.w}, a4[4] = {al.x, al.y, al.z, al.w};
+                    const uint32_t B4[4] = {bh.x, bh.y, bh.z, bh.w}, b4[4] = {bl.x, bl.y, bl.z, bl.w};
 #pragma unroll
-            for (int i = 0; i < NPAD / 64; ++i) {
-                const uint32_t o = (tid + 512 * i) * 16;
-                const uint4 ah = lds16(sS + o), al = lds16(sS + PLANE + o);
-                const uint4 bh = lds16(sS + 2 * PLANE + o), bl = lds16(sS + 3 * PLANE + o);
-                const uint32_t A4[4] = {ah.x, ah.y, ah.z, ah.w}, a4[4] = {al.x, al.y, al.z, al.w};
-                const uint32_t B4[4] = {bh.x, bh.y, bh.z, bh.w}, b4[4] = {bl.x, bl.y, bl.z, bl.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    dot = fmaf(umma::lo_f(A4[q]) + umma::lo_f(a4[q]), umma::lo_f(B4[q]) + umma::lo_f(b4[q]), dot);
-                    dot = fmaf(umma::hi_f(A4[q]) + umma::hi_f(a4[q]), umma::hi_f(B4[q]) + umma::hi_f(b4[q]), dot);
+                    for (int q = 0; q < 4; ++q) {
+                        dot = fmaf(umma::lo_f(A4[q]) + umma::lo_f(a4[q]), umma::lo_f(B4[q]) + umma::lo_f(b4[q]), dot);
+                        dot = fmaf(umma::hi_f(A4[q]) + umma::hi_f(a4[q]), umma::hi_f(B4[q]) + umma::hi_f(b4[q]), dot);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ss_free);
+                dot = warp_sum(dot);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ss_free);
-            dot = warp_sum(dot);
             if (it >= 2) wait(&fin[it & 1], (it >> 1) - 1);
 
             wait(&ud[it & 1], it >> 1);
-            const float ds = tb[kTabD + row], ls = tb[kTabL + row];
+            const float ds = tb[kTabD + row], ls = tb[kTabL + row], lls = tb[kTabLl + row];
             wait(&dm, it);
             umma::fence_after();
             float own = 0.0f;
@@ -420,9 +424,13 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
                 } else {
                     const float4 la = *reinterpret_cast<const float4 *>(tb + kTabL + 32 * j + 8 * cg);
                     const float4 lb = *reinterpret_cast<const float4 *>(tb + kTabL + 32 * j + 8 * cg + 4);
+                    const float4 ra = *reinterpret_cast<const float4 *>(tb + kTabLl + 32 * j + 8 * cg);
+                    const float4 rb = *reinterpret_cast<const float4 *>(tb + kTabLl + 32 * j + 8 * cg + 4);
                     const float lt[8] = {la.x, la.y, la.z, la.w, lb.x, lb.y, lb.z, lb.w};
+                    const float lr[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) L[c] = 8 * cg + c >= lane ? ex2_approx(lt[c] - ls) : 0.0f;
+                    for (int c = 0; c < 8; ++c)
+                        L[c] = 8 * cg + c >= lane ? ex2_approx((lt[c] - ls) + (lr[c] - lls)) : 0.0f;
                 }
                 umma::wait_ld();
                 float wd[8];
@@ -447,9 +455,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
                     k2 = add2(k2, wl);
                     upk2(mul2(wl, d2), wd[c], wd[c + 1]);
                 }
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
-                             :: "r"(kMt + me + 16 * j + 4 * cg), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                             : "memory");
+                umma::st4(kMt + me + 16 * j + 4 * cg, w);
                 const float r = reduce8(wd, lane);
                 if (lane < 8) s.r[wi][32 * j + 8 * cg + lane] = r;
             }
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
                 sk = warp_sum(sk);
                 if (lane == 0) {
                     s.skip[warp] = sk;
-                    s.dot[warp] = dot;
+                    if (wi >= 2) s.dot[warp] = dot;
                 }
                 wait(&du, it);
                 umma::fence_after();
@@ -535,14 +541,20 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             __syncwarp();
             if (lane == 0) mbar_arrive(&epi[it & 1]);
         }
-        // dG^T of the panels, rounded once, as the next kernel's left operand
-        bf16 *tile = a.dg + ((slot * z.G + g) * a.ranges + range) * (int64_t)kC * kC;
+        // dG^T of the panels in two planes, as the next kernel's left operands
+        char *tile = reinterpret_cast<char *>(a.dg + ((slot * z.G + g) * a.ranges + range) * (int64_t)(2 * kC * kC));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = 4 * j + cg;
-            const uint4 v = make_uint4(umma::pack(dg[j][0], dg[j][1]), umma::pack(dg[j][2], dg[j][3]),
-                                       umma::pack(dg[j][4], dg[j][5]), umma::pack(dg[j][6], dg[j][7]));
-            *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(tile) + (c / 8) * umma::kPanel + umma::piece(row, c % 8)) = v;
+            char *to = tile + (c / 8) * umma::kPanel + umma::piece(row, c % 8);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hi[i] = umma::pack(dg[j][2 * i], dg[j][2 * i + 1]);
+                lo[i] = umma::pack(dg[j][2 * i] - umma::lo_f(hi[i]), dg[j][2 * i + 1] - umma::hi_f(hi[i]));
+            }
+            *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(to + 2 * umma::kPanel) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
     umma::fence_before();
@@ -664,7 +676,7 @@ __global__ void __launch_bounds__(kBcThreads) head_bwd_bc_kernel(BwdArgs a, cons
             const uint64_t cm = umma::desc_mn(stages, 0, umma::kPanel);
             const uint64_t bm = umma::desc_mn(stages + BP * umma::kPanel, 0, umma::kPanel);
             const uint64_t gk = umma::desc_k(stages + STAGE, 0), gm = umma::desc_mn(stages + STAGE, 0, umma::kPanel);
-            for (int r = 0; r < a.ranges; ++r) {
+            for (int r = 0; r < 2 * a.ranges; ++r) {
                 wait(&last_in, r);
                 umma::fence_after();
 #pragma unroll
@@ -715,8 +727,8 @@ __global__ void __launch_bounds__(kBcThreads) head_bwd_bc_kernel(BwdArgs a, cons
         load_tile<NPAD, 512, VEC>(stages, a.C + ck.start * a.bc_stride + (int64_t)g * z.N, a.bc_stride, len, z.N, tid);
         load_tile<NPAD, 512, VEC>(stages + BP * umma::kPanel, a.B + ck.start * a.bc_stride + (int64_t)g * z.N,
                                   a.bc_stride, len, z.N, tid);
-        for (int r = 0; r < a.ranges; ++r) {
-            const bf16 *tile = a.dg + ((slot * z.G + g) * a.ranges + r) * (int64_t)kC * kC;
+        for (int r = 0; r < 2 * a.ranges; ++r) {
+            const bf16 *tile = a.dg + ((slot * z.G + g) * a.ranges * 2 + r) * (int64_t)kC * kC;
             if (r > 0) wait(&last_out, r - 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -728,7 +740,7 @@ __global__ void __launch_bounds__(kBcThreads) head_bwd_bc_kernel(BwdArgs a, cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&last_in);
         }
-        wait(&last_out, a.ranges - 1);
+        wait(&last_out, 2 * a.ranges - 1);
         umma::fence_after();
         add(0, 1.0f, dc);
         add(128, 1.0f, db);
@@ -806,11 +818,12 @@ BwdLayout bwd_layout(const Dims &z)
     // ranges as leave about three CTAs an SM
     int64_t heads = z.H / z.G, per = slots * z.G * heads / (148 * 3);
     per = per < 1 ? 1 : per > heads ? heads : per;
-    l.per = (int)per * z.np;
     l.ranges = (int)((heads + per - 1) / per);
+    l.per = (int)((heads + l.ranges - 1) / l.ranges) * z.np;  // ranges of like size
+    l.ranges = (z.npan + l.per - 1) / l.per;
     l.dS = l.walk.total;
     l.dg = l.dS + marks;
-    l.part = l.dg + up256((size_t)slots * z.G * l.ranges * kC * kC * 2);
+    l.part = l.dg + up256((size_t)slots * z.G * l.ranges * kC * kC * 4);
     l.total = l.part + up256((size_t)slots * z.H * 3 * 4);
     return l;
 }

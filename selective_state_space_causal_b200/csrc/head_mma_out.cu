@@ -341,6 +341,8 @@ cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t st, int *launches
     int64_t per = slots * z.G * z.npan / (148 * 4);
     per = per < 2 ? 2 : per > 24 ? 24 : per;
     if (per > z.npan) per = z.npan;
+    const int64_t ranges = (z.npan + per - 1) / per;
+    per = (z.npan + ranges - 1) / ranges;  // ranges of like size
     OutArgs o{z, static_cast<const bf16 *>(a.u), static_cast<const bf16 *>(a.B), static_cast<const bf16 *>(a.C),
               a.u_stride, a.bc_stride, a.Dskip, tab, marks, static_cast<bf16 *>(a.y), (int)per, vec16(a.y, a.P, a.P)};
     ++*launches;

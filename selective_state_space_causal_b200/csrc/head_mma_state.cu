@@ -22,6 +22,13 @@ __device__ int g_status;
 
 namespace {
 
+// 2^x with the argument's rounding to fp32 made good: at x = -20 it alone is 1e-6.
+__device__ __forceinline__ float exp2_of(double x)
+{
+    const float h = (float)x, r = ex2_approx(h);
+    return fmaf(r, (float)(x - (double)h) * 0.6931471806f, r);
+}
+
 // One block per (chunk slot, 32 heads).
 __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *delta, int64_t stride,
                                                          const float *A, const float *bias,
@@ -66,19 +73,20 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
         pre -= sum;
         const int blk = lane / 8;
         const double r = blk == 0 ? 0.0 : blk == 1 ? r1 : blk == 2 ? r2 : r3;
-        float lv[4], ev[4], wv[4], wn[4], el[4], c1[4], c2[4], c3[4];
+        float lv[4], ll[4], ev[4], wv[4], wn[4], el[4], c1[4], c2[4], c3[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const double c = pre + run[j];
             lv[j] = (float)(c - r);
-            ev[j] = ex2_approx((float)c);
-            wn[j] = ex2_approx((float)(last - c));
+            ll[j] = (float)(c - r - (double)lv[j]);
+            ev[j] = exp2_of(c);
+            wn[j] = exp2_of(last - c);
             wv[j] = dv[j] * wn[j];
-            el[j] = ex2_approx(lv[j]);
+            el[j] = exp2_of(c - r);
             const float f = backward ? 1.0f : dv[j];
-            c1[j] = f * ex2_approx((float)(r1 - c));
-            c2[j] = f * ex2_approx((float)(r2 - c));
-            c3[j] = f * ex2_approx((float)(r3 - c));
+            c1[j] = f * exp2_of(r1 - c);
+            c2[j] = f * exp2_of(r2 - c);
+            c3[j] = f * exp2_of(r3 - c);
         }
         float *q = tab + (slot * z.H + h0 + i) * kTab;
         auto put = [&](int at, const float (&v)[4]) {
@@ -91,6 +99,7 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
         if (backward) {
             put(kTabWn, wn);
             put(kTabEl, el);
+            put(kTabLl, ll);
         }
         if (blk < 1) put(col_at(1), c1);
         if (blk < 2) put(col_at(2), c2);
@@ -132,7 +141,7 @@ constexpr int state_smem()
     return 1024 + kStages * state_stage<NPAD>();
 }
 
-// One CTA has one or two panels of one group and walks a segment's chunks. The warps have
+// One CTA has two panels of one group and walks a segment's chunks. The warps have
 // roles, so that loads, conversion, matrix instructions and state updates of
 // neighbouring chunks run at the same time (with all warps in step, each phase's
 // latency was exposed: 5500 clocks a chunk against 1536 of matrix instructions):
@@ -159,9 +168,9 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     // whole sequences go longest first: a long one started last would run almost alone
     const int64_t slot = a.order ? a.order[blockIdx.y] : blockIdx.y;
-    const int per_group = (z.npan + a.width - 1) / a.width;
-    const int g = blockIdx.x / per_group, pan0 = blockIdx.x % per_group * a.width;
-    const int np = min(a.width, z.npan - pan0);  // panels of this CTA
+    const int per_group = (z.npan + 1) / 2;
+    const int g = blockIdx.x / per_group, pan0 = blockIdx.x % per_group * 2;
+    const int np = min(2, z.npan - pan0);  // panels of this CTA
     const ChunkRef sg = find_chunk(z.cu, z.S, z.tok, a.span, slot);
     if (sg.len == 0 && (sg.k != 0 || a.segment != 0)) return;
     const int nchunk = (sg.len + kC - 1) / kC;
@@ -476,7 +485,7 @@ cudaError_t launch_walk(const StateArgs &a, cudaStream_t st, int *launches)
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e != cudaSuccess)
         return e;
-    const dim3 grid((unsigned)(a.z.G * ((a.z.npan + a.width - 1) / a.width)),
+    const dim3 grid((unsigned)(a.z.G * ((a.z.npan + 1) / 2)),
                     (unsigned)head_slots(a.z.tok, a.z.S, a.span));
     CUtensorMap xmap{}, bmap{};
     if (VEC && a.z.tok > 0 &&
@@ -496,9 +505,6 @@ cudaError_t states(StateArgs a, bool split, bool vec, cudaStream_t st, int *laun
         return vec ? launch_walk<NPAD, REV, PLANES, true>(a, st, launches)
                    : launch_walk<NPAD, REV, PLANES, false>(a, st, launches);
     };
-    // one panel a CTA where two would leave SMs without one: a chunk then takes about 0.6 of
-    // the time, at the price of loading b twice
-    a.width = a.z.S * a.z.G * ((a.z.npan + 1) / 2) < 148 && !split ? 1 : 2;
     if (split) a.order = nullptr;
     else if (a.order) {
         if (cudaError_t e = launch_seq_order(a.z.cu, a.z.S, a.z.tok, a.order, st); e != cudaSuccess) return e;

@@ -1,4 +1,5 @@
-// head_scan.cu -- the scan with one decay per head, token by token, and its backward.
+// head_scan.cu -- the scan with one decay per head in fp32, token by token, its backward,
+// and the choice between these kernels and the tensor-core ones (bf16).
 //
 // head_recurrent_kernel walks a sequence with a 64-row tile of one head's state
 // in registers (the forward, or the reverse walk of the state's gradient);
@@ -16,10 +17,9 @@ namespace {
 constexpr int kQ = 32;   // tokens per chunk
 constexpr int kPT = 64;  // state rows per CTA
 
-template <typename T>
 struct RecArgs {
-    const T *x;  // u, or dy in the reverse walk
-    const T *B, *C, *delta;
+    const float *x;  // u, or dy in the reverse walk
+    const float *B, *C, *delta;
     int64_t x_stride, bc_stride, delta_stride;
     const float *A, *Dskip, *dt_bias;
     int softplus;
@@ -27,7 +27,7 @@ struct RecArgs {
     const int32_t *cu;
     int64_t S, tok;
     int H, P, G, N;
-    T *y;           // forward output, or nullptr
+    float *y;           // forward output, or nullptr
     float *marks;   // state before each chunk in walking order, or nullptr
     float *final_;  // h_final or dh0, or nullptr
 };
@@ -35,8 +35,8 @@ struct RecArgs {
 // Four lanes share a state row, each with NV float4 of its columns; a lane has two
 // rows. What it reads per token (B, C and u from shared memory) bounds it: 16 wide
 // shared loads for 128 fused multiply-adds at N = 128.
-template <typename T, int NV, bool REV>
-__global__ void __launch_bounds__(128) head_recurrent_kernel(RecArgs<T> a)
+template <int NV, bool REV>
+__global__ void __launch_bounds__(128) head_recurrent_kernel(RecArgs a)
 {
     constexpr int NP = NV * 16;
     __shared__ __align__(16) float sB[kQ][NP], sC[kQ][NP];
@@ -87,15 +87,15 @@ __global__ void __launch_bounds__(128) head_recurrent_kernel(RecArgs<T> a)
         for (int i = tid; i < len * NP; i += 128) {
             const int t = i / NP, n = i % NP;
             const int64_t at = (t0 + t) * a.bc_stride + (int64_t)g * a.N + n;
-            if (!REV) sB[t][n] = n < a.N ? to_f32(a.B[at]) : 0.0f;
-            sC[t][n] = n < a.N ? to_f32(a.C[at]) : 0.0f;
+            if (!REV) sB[t][n] = n < a.N ? a.B[at] : 0.0f;
+            sC[t][n] = n < a.N ? a.C[at] : 0.0f;
         }
         for (int i = tid; i < len * kPT; i += 128) {
             const int t = i / kPT, p = i % kPT;
-            sx[t][p] = p < rows ? to_f32(a.x[(t0 + t) * a.x_stride + (int64_t)h * a.P + p0 + p]) : 0.0f;
+            sx[t][p] = p < rows ? a.x[(t0 + t) * a.x_stride + (int64_t)h * a.P + p0 + p] : 0.0f;
         }
         if (tid < len) {
-            const float d = head_step(to_f32(a.delta[(t0 + tid) * a.delta_stride + h]) + bias, a.softplus);
+            const float d = head_step(a.delta[(t0 + tid) * a.delta_stride + h] + bias, a.softplus);
             const float lg = d * Ah;
             sd[tid] = d;
             sa[tid] = expf(lg < kHeadMinLog ? kHeadMinLog : lg);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(128) head_recurrent_kernel(RecArgs<T> a)
             for (int i = tid; i < len * kPT; i += 128) {
                 const int t = i / kPT, p = i % kPT;
                 if (p < rows)
-                    a.y[((t0 + t) * a.H + h) * (int64_t)a.P + p0 + p] = from_f32<T>(sx[t][p]);
+                    a.y[((t0 + t) * a.H + h) * (int64_t)a.P + p0 + p] = sx[t][p];
             }
         }
     }
@@ -195,9 +195,8 @@ __device__ __forceinline__ void small_gemm(int M, int N, int K, FA fa, FB fb, FO
     }
 }
 
-template <typename T>
 struct ChunkBwdArgs {
-    const T *u, *B, *C, *delta, *dy;
+    const float *u, *B, *C, *delta, *dy;
     int64_t u_stride, bc_stride, delta_stride;
     const float *A, *Dskip, *dt_bias;
     int softplus;
@@ -205,7 +204,7 @@ struct ChunkBwdArgs {
     int64_t S, tok;
     int H, P, G, N;
     const float *S0, *dS;  // per chunk: start state, gradient of the end state
-    T *du, *ddelta, *dB, *dC;
+    float *du, *ddelta, *dB, *dC;
     float *part;  // (slot, H, 3): this chunk's share of dA, ddt_bias, dDskip
 };
 
@@ -217,8 +216,7 @@ int chunk_bwd_floats(int N)
     return 2 * kQ + 4 * kQ * ns + 2 * kPT * ns + 3 * kQ * (kPT + 1) + 3 * kQ * (kQ + 1) + 5 * kQ + 64;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
+__global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs a)
 {
     extern __shared__ __align__(16) float smem[];
     const int tid = threadIdx.x, N = a.N, ns = N | 1, ps = kPT + 1, qs = kQ + 1;
@@ -240,8 +238,8 @@ __global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
     for (int i = tid; i < kQ * N; i += 256) {
         const int t = i / N, n = i % N;
         const int64_t at = (ck.start + t) * a.bc_stride + (int64_t)g * N + n;
-        sB[t * ns + n] = t < len ? to_f32(a.B[at]) : 0.0f;
-        sC[t * ns + n] = t < len ? to_f32(a.C[at]) : 0.0f;
+        sB[t * ns + n] = t < len ? a.B[at] : 0.0f;
+        sC[t * ns + n] = t < len ? a.C[at] : 0.0f;
         sdB[t * ns + n] = 0.0f;
         sdC[t * ns + n] = 0.0f;
     }
@@ -256,7 +254,7 @@ __global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
         __syncthreads();
         if (tid < 32) {
             const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-            const float rw = tid < len ? to_f32(a.delta[(ck.start + tid) * a.delta_stride + h]) + bias : 0.0f;
+            const float rw = tid < len ? (a.delta[(ck.start + tid) * a.delta_stride + h]) + bias : 0.0f;
             const float dt = tid < len ? head_step(rw, a.softplus) : 0.0f;
             float lg = dt * Ah;
             lg = lg < kHeadMinLog ? kHeadMinLog : lg;
@@ -282,8 +280,8 @@ __global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
                 const int t = i / kPT, p = i % kPT;
                 const bool in = t < len && p < rows;
                 const int64_t tk = ck.start + t;
-                const float uv = in ? to_f32(a.u[tk * a.u_stride + (int64_t)h * a.P + p0 + p]) : 0.0f;
-                const float yv = in ? to_f32(a.dy[(tk * a.H + h) * a.P + p0 + p]) : 0.0f;
+                const float uv = in ? a.u[tk * a.u_stride + (int64_t)h * a.P + p0 + p] : 0.0f;
+                const float yv = in ? a.dy[(tk * a.H + h) * a.P + p0 + p] : 0.0f;
                 U[t * ps + p] = uv;
                 Y[t * ps + p] = yv;
                 dskip = fmaf(uv, yv, dskip);
@@ -332,7 +330,7 @@ __global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
                            if (s < len && p < rows) {
                                const float w = expf((float)(c[len - 1] - c[s]));
                                const float o = fmaf(d[s], v + w * V[s * ps + p], skip * Y[s * ps + p]);
-                               a.du[((ck.start + s) * a.H + h) * (int64_t)a.P + p0 + p] = from_f32<T>(o);
+                               a.du[((ck.start + s) * a.H + h) * (int64_t)a.P + p0 + p] = o;
                            }
                        });
             __syncthreads();
@@ -398,7 +396,7 @@ __global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
             float pa = 0.0f, pb = 0.0f;
             if (tid < len) {
                 const float gv = (col[tid] + own[tid] + Ah * (float)dg) * head_step_grad(raw[tid], a.softplus);
-                a.ddelta[(ck.start + tid) * a.H + h] = from_f32<T>(gv);
+                a.ddelta[(ck.start + tid) * a.H + h] = gv;
                 pa = d[tid] * (float)dg;
                 pb = gv;
             }
@@ -419,8 +417,8 @@ __global__ void __launch_bounds__(256) head_bwd_chunk_kernel(ChunkBwdArgs<T> a)
     for (int i = tid; i < len * N; i += 256) {
         const int t = i / N, n = i % N;
         const int64_t at = ((ck.start + t) * a.G + g) * (int64_t)N + n;
-        a.dB[at] = from_f32<T>(sdB[t * ns + n]);
-        a.dC[at] = from_f32<T>(sdC[t * ns + n]);
+        a.dB[at] = sdB[t * ns + n];
+        a.dC[at] = sdC[t * ns + n];
     }
 }
 
@@ -447,15 +445,14 @@ __global__ void __launch_bounds__(256) head_reduce_kernel(const float *part, int
     }
 }
 
-template <typename T>
-RecArgs<T> rec_args(const HeadScanArgs &a, bool rev)
+RecArgs rec_args(const HeadScanArgs &a, bool rev)
 {
-    RecArgs<T> r;
-    r.x = static_cast<const T *>(rev ? a.dy : a.u);
+    RecArgs r;
+    r.x = static_cast<const float *>(rev ? a.dy : a.u);
     r.x_stride = rev ? a.H * a.P : a.u_stride;
-    r.B = static_cast<const T *>(a.B);
-    r.C = static_cast<const T *>(a.C);
-    r.delta = static_cast<const T *>(a.delta);
+    r.B = static_cast<const float *>(a.B);
+    r.C = static_cast<const float *>(a.C);
+    r.delta = static_cast<const float *>(a.delta);
     r.bc_stride = a.bc_stride;
     r.delta_stride = a.delta_stride;
     r.A = a.A;
@@ -476,30 +473,28 @@ RecArgs<T> rec_args(const HeadScanArgs &a, bool rev)
     return r;
 }
 
-template <typename T, bool REV>
-cudaError_t launch_recurrent(const RecArgs<T> &r, cudaStream_t stream, int *launches)
+template <bool REV>
+cudaError_t launch_recurrent(const RecArgs &r, cudaStream_t stream, int *launches)
 {
     const dim3 grid((unsigned)r.S, (unsigned)(r.H * ((r.P + kPT - 1) / kPT)));
-    if (r.N <= 16) head_recurrent_kernel<T, 1, REV><<<grid, 128, 0, stream>>>(r);
-    else if (r.N <= 32) head_recurrent_kernel<T, 2, REV><<<grid, 128, 0, stream>>>(r);
-    else if (r.N <= 64) head_recurrent_kernel<T, 4, REV><<<grid, 128, 0, stream>>>(r);
-    else head_recurrent_kernel<T, 8, REV><<<grid, 128, 0, stream>>>(r);
+    if (r.N <= 16) head_recurrent_kernel<1, REV><<<grid, 128, 0, stream>>>(r);
+    else if (r.N <= 32) head_recurrent_kernel<2, REV><<<grid, 128, 0, stream>>>(r);
+    else if (r.N <= 64) head_recurrent_kernel<4, REV><<<grid, 128, 0, stream>>>(r);
+    else head_recurrent_kernel<8, REV><<<grid, 128, 0, stream>>>(r);
     ++*launches;
     return cudaGetLastError();
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-template <typename T>
 cudaError_t fwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 {
-    RecArgs<T> r = rec_args<T>(a, false);
-    r.y = static_cast<T *>(a.y);
+    RecArgs r = rec_args(a, false);
+    r.y = static_cast<float *>(a.y);
     r.final_ = a.h_final;
-    return launch_recurrent<T, false>(r, stream, launches);
+    return launch_recurrent<false>(r, stream, launches);
 }
 
-template <typename T>
 cudaError_t bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 {
     const int64_t slots = head_slots(a.tok, a.S, kQ);
@@ -507,19 +502,19 @@ cudaError_t bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
     char *ws = static_cast<char *>(a.workspace);
     float *S0 = reinterpret_cast<float *>(ws), *dS = reinterpret_cast<float *>(ws + state);
     float *part = reinterpret_cast<float *>(ws + 2 * state);
-    RecArgs<T> r = rec_args<T>(a, false);
+    RecArgs r = rec_args(a, false);
     r.marks = S0;
-    if (cudaError_t e = launch_recurrent<T, false>(r, stream, launches); e != cudaSuccess) return e;
-    r = rec_args<T>(a, true);
+    if (cudaError_t e = launch_recurrent<false>(r, stream, launches); e != cudaSuccess) return e;
+    r = rec_args(a, true);
     r.marks = dS;
     r.final_ = a.dh0;
-    if (cudaError_t e = launch_recurrent<T, true>(r, stream, launches); e != cudaSuccess) return e;
-    ChunkBwdArgs<T> b;
-    b.u = static_cast<const T *>(a.u);
-    b.B = static_cast<const T *>(a.B);
-    b.C = static_cast<const T *>(a.C);
-    b.delta = static_cast<const T *>(a.delta);
-    b.dy = static_cast<const T *>(a.dy);
+    if (cudaError_t e = launch_recurrent<true>(r, stream, launches); e != cudaSuccess) return e;
+    ChunkBwdArgs b;
+    b.u = static_cast<const float *>(a.u);
+    b.B = static_cast<const float *>(a.B);
+    b.C = static_cast<const float *>(a.C);
+    b.delta = static_cast<const float *>(a.delta);
+    b.dy = static_cast<const float *>(a.dy);
     b.u_stride = a.u_stride;
     b.bc_stride = a.bc_stride;
     b.delta_stride = a.delta_stride;
@@ -536,17 +531,17 @@ cudaError_t bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
     b.N = (int)a.N;
     b.S0 = S0;
     b.dS = dS;
-    b.du = static_cast<T *>(a.du);
-    b.ddelta = static_cast<T *>(a.ddelta);
-    b.dB = static_cast<T *>(a.dB);
-    b.dC = static_cast<T *>(a.dC);
+    b.du = static_cast<float *>(a.du);
+    b.ddelta = static_cast<float *>(a.ddelta);
+    b.dB = static_cast<float *>(a.dB);
+    b.dC = static_cast<float *>(a.dC);
     b.part = part;
     const int bytes = chunk_bwd_floats(b.N) * 4;
-    if (cudaError_t e = cudaFuncSetAttribute(head_bwd_chunk_kernel<T>,
+    if (cudaError_t e = cudaFuncSetAttribute(head_bwd_chunk_kernel,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         e != cudaSuccess)
         return e;
-    head_bwd_chunk_kernel<T><<<dim3((unsigned)slots, (unsigned)a.G), 256, bytes, stream>>>(b);
+    head_bwd_chunk_kernel<<<dim3((unsigned)slots, (unsigned)a.G), 256, bytes, stream>>>(b);
     ++*launches;
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     return launch_head_reduce(part, slots, b.H, a.dA, a.ddt_bias, a.dDskip, stream, launches);
@@ -586,13 +581,13 @@ size_t head_scan_bwd_workspace_bytes(int64_t tok, int64_t H, int64_t P, int64_t 
 cudaError_t launch_head_scan(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 {
     return a.dtype == DType::BF16 ? hm::launch_forward(a, stream, launches)
-                                  : fwd<float>(a, stream, launches);
+                                  : fwd(a, stream, launches);
 }
 
 cudaError_t launch_head_scan_bwd(const HeadScanArgs &a, cudaStream_t stream, int *launches)
 {
     return a.dtype == DType::BF16 ? hm::launch_backward(a, stream, launches)
-                                  : bwd<float>(a, stream, launches);
+                                  : bwd(a, stream, launches);
 }
 
 }  // namespace ssm
