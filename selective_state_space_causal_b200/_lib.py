@@ -136,7 +136,8 @@ def _stream(stream):
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
 
-    return torch.cuda.current_stream().cuda_stream
+    # the raw handle: building torch's stream object costs more than the rest of a small call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def ssm_last_error() -> str:

@@ -137,7 +137,7 @@ constexpr int64_t kMark = (int64_t)64 * NPAD;  // elements of one plane
 
 // Scratch that one call needs, carved from the workspace in this order.
 struct Layout {
-    size_t tab, seg, segdec, marks, order, total;
+    size_t tab, seg, segdec, marks, order, span, total;
 };
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -152,25 +152,37 @@ struct StateArgs {
     const float *init;  // (S, H, P, N) or nullptr
     float *final_;      // (S, H, P, N) or nullptr
     bf16 *marks;        // state before each chunk in walking order
-    int64_t span;       // tokens of a segment (a multiple of kC)
-    float *seg;         // split walks: (segment slot, panel, NPAD / 4, 64, 4) end, then start states
-    float *segdec;      // (segment slot, head): the segment's decay
+    float *seg;         // (segment slot, panel, NPAD / 4, 64, 4): segments' end states from zero
+    float *segdec;      // (segment slot, head): a segment's decay
     int32_t *order;     // room for the sequences' order, or nullptr
-    int segment = 0;    // 0: whole sequences; 1, 2: the passes of a split walk
+    const int64_t *asked;  // where the table kernel left the span, for Plan::kAsk
+    int64_t span = 0;   // tokens of a segment (a multiple of kC)
+    bool first = false; // the first of a cut walk's two passes
 };
+
+// How sequences are walked: whole, cut into segments of `span` tokens, or cut if the
+// longest has more than `limit` chunks, which the device finds out.
+struct Plan {
+    enum Mode { kWhole, kCut, kAsk } mode;
+    int64_t span;
+    int limit;
+};
+constexpr int64_t kNoSpan = (int64_t)1 << 31;  // longer than any sequence
+// `known`: the lengths are those of dense rows. A workspace has room for either plan, since
+// its size is asked for without cu_seqlens.
+Plan plan_of(const Dims &z, bool known);
+inline bool lengths_known(const Dims &z) { return !z.cu; }
 
 // Steps and running decays of every chunk.
 cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, bool backward,
-                          cudaStream_t stream, int *launches);
+                          const Plan &plan, int64_t *span, cudaStream_t stream, int *launches);
 // The states before every chunk (forward) or the gradients of the states after every
 // chunk (reverse), `planes` bf16 planes each.
-cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, bool vec,
+cudaError_t launch_states(const StateArgs &a, bool rev, int planes, const Plan &plan, bool vec,
                           cudaStream_t stream, int *launches);
 // Workspace of the tables and of one walk's segments and marks.
-Layout layout_of(const Dims &z, int planes, int64_t span, bool split);
+Layout layout_of(const Dims &z, int planes, const Plan &plan);
 Dims dims_of(const HeadScanArgs &a);
-// Tokens per segment of the walk, and whether walks are split.
-int64_t segment_span(const Dims &z, bool *split);
 
 cudaError_t launch_backward(const HeadScanArgs &a, cudaStream_t stream, int *launches);
 size_t backward_bytes(const Dims &z);

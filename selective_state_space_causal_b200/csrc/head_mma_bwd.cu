@@ -803,15 +803,14 @@ struct BwdLayout {
     Layout walk;
     size_t dS, dg, part, total;
     int per, ranges;
-    bool split;
-    int64_t span;
+    Plan plan;
 };
 
-BwdLayout bwd_layout(const Dims &z)
+BwdLayout bwd_layout(const Dims &z, bool known)
 {
     BwdLayout l;
-    l.span = segment_span(z, &l.split);
-    l.walk = layout_of(z, 2, l.span, l.split);
+    l.plan = plan_of(z, known);
+    l.walk = layout_of(z, 2, l.plan);
     const int64_t slots = head_slots(z.tok, z.S, kC);
     const size_t marks = l.walk.order - l.walk.marks;
     // whole heads per CTA; G^T and the rounded dG^T are shared by a CTA's panels, so as few
@@ -830,28 +829,33 @@ BwdLayout bwd_layout(const Dims &z)
 
 }  // namespace
 
-size_t backward_bytes(const Dims &z) { return bwd_layout(z).total; }
+size_t backward_bytes(const Dims &z)
+{
+    const size_t dense = bwd_layout(z, true).total, packed = bwd_layout(z, false).total;
+    return dense > packed ? dense : packed;
+}
 
 cudaError_t launch_backward(const HeadScanArgs &a, cudaStream_t st, int *launches)
 {
     const Dims z = dims_of(a);
-    const BwdLayout l = bwd_layout(z);
+    const BwdLayout l = bwd_layout(z, lengths_known(z));
     char *ws = static_cast<char *>(a.workspace);
     float *tab = reinterpret_cast<float *>(ws + l.walk.tab);
     bf16 *S0 = reinterpret_cast<bf16 *>(ws + l.walk.marks), *dS = reinterpret_cast<bf16 *>(ws + l.dS);
     float *seg = reinterpret_cast<float *>(ws + l.walk.seg), *segdec = reinterpret_cast<float *>(ws + l.walk.segdec);
+    int64_t *span = reinterpret_cast<int64_t *>(ws + l.walk.span);
     int32_t *order = a.cu && a.S > 1 ? reinterpret_cast<int32_t *>(ws + l.walk.order) : nullptr;
     float *part = reinterpret_cast<float *>(ws + l.part);
-    if (cudaError_t e = launch_tables(a, z, tab, true, st, launches); e != cudaSuccess) return e;
+    if (cudaError_t e = launch_tables(a, z, tab, true, l.plan, span, st, launches); e != cudaSuccess) return e;
     const int64_t row = a.H * a.P;
     const bool bc_vec = vec16(a.B, a.bc_stride, a.N) && vec16(a.C, a.bc_stride, a.N);
     const bool vec = bc_vec && vec16(a.u, a.u_stride, a.P) && vec16(a.dy, row, a.P);
     const bf16 *u = static_cast<const bf16 *>(a.u), *dy = static_cast<const bf16 *>(a.dy);
     const bf16 *B = static_cast<const bf16 *>(a.B), *C = static_cast<const bf16 *>(a.C);
-    StateArgs s{z, u, a.u_stride, B, a.bc_stride, tab, a.h0, nullptr, S0, l.span, seg, segdec, order};
-    if (cudaError_t e = launch_states(s, false, 2, l.split, vec, st, launches); e != cudaSuccess) return e;
-    StateArgs r{z, dy, row, C, a.bc_stride, tab, a.dh_final, a.dh0, dS, l.span, seg, segdec, order};
-    if (cudaError_t e = launch_states(r, true, 2, l.split, vec, st, launches); e != cudaSuccess) return e;
+    StateArgs s{z, u, a.u_stride, B, a.bc_stride, tab, a.h0, nullptr, S0, seg, segdec, order, span};
+    if (cudaError_t e = launch_states(s, false, 2, l.plan, vec, st, launches); e != cudaSuccess) return e;
+    StateArgs r{z, dy, row, C, a.bc_stride, tab, a.dh_final, a.dh0, dS, seg, segdec, order, span};
+    if (cudaError_t e = launch_states(r, true, 2, l.plan, vec, st, launches); e != cudaSuccess) return e;
     const int64_t slots = head_slots(z.tok, z.S, kC);
     BwdArgs b{z, u, dy, B, C, static_cast<const bf16 *>(a.delta), a.u_stride, a.bc_stride, a.delta_stride,
               a.A, a.Dskip, a.dt_bias, a.delta_softplus, tab, S0, dS, static_cast<bf16 *>(a.du),

@@ -322,19 +322,19 @@ cudaError_t out(const OutArgs &a, int64_t slots, cudaStream_t st)
 cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t st, int *launches)
 {
     const Dims z = dims_of(a);
-    bool split;
-    const int64_t span = segment_span(z, &split);
-    const Layout l = layout_of(z, 1, span, split);
+    const Plan plan = plan_of(z, lengths_known(z));
+    const Layout l = layout_of(z, 1, plan);
     char *ws = static_cast<char *>(a.workspace);
     float *tab = reinterpret_cast<float *>(ws + l.tab);
     bf16 *marks = reinterpret_cast<bf16 *>(ws + l.marks);
-    if (cudaError_t e = launch_tables(a, z, tab, false, st, launches); e != cudaSuccess) return e;
+    int64_t *span = reinterpret_cast<int64_t *>(ws + l.span);
+    if (cudaError_t e = launch_tables(a, z, tab, false, plan, span, st, launches); e != cudaSuccess) return e;
     const bool vec = vec16(a.B, a.bc_stride, a.N) && vec16(a.C, a.bc_stride, a.N) && vec16(a.u, a.u_stride, a.P);
     StateArgs s{z, static_cast<const bf16 *>(a.u), a.u_stride, static_cast<const bf16 *>(a.B), a.bc_stride,
-                tab, a.h0, a.h_final, marks, span, reinterpret_cast<float *>(ws + l.seg),
+                tab, a.h0, a.h_final, marks, reinterpret_cast<float *>(ws + l.seg),
                 reinterpret_cast<float *>(ws + l.segdec),
-                a.cu && a.S > 1 ? reinterpret_cast<int32_t *>(ws + l.order) : nullptr};
-    if (cudaError_t e = launch_states(s, false, 1, split, vec, st, launches); e != cudaSuccess) return e;
+                a.cu && a.S > 1 ? reinterpret_cast<int32_t *>(ws + l.order) : nullptr, span};
+    if (cudaError_t e = launch_states(s, false, 1, plan, vec, st, launches); e != cudaSuccess) return e;
     if (a.tok == 0) return cudaSuccess;
     const int64_t slots = head_slots(z.tok, z.S, kC);
     // G is made once per CTA: as many panels a CTA as leave about four CTAs an SM
@@ -352,9 +352,9 @@ cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t st, int *launches
 
 size_t forward_bytes(const Dims &z)
 {
-    bool split;
-    const int64_t span = segment_span(z, &split);
-    return layout_of(z, 1, span, split).total;
+    // asked for without cu_seqlens: room for the walk of dense rows and of packed ones
+    const size_t dense = layout_of(z, 1, plan_of(z, true)).total, packed = layout_of(z, 1, plan_of(z, false)).total;
+    return dense > packed ? dense : packed;
 }
 
 }  // namespace hm

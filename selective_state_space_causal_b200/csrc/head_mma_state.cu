@@ -32,11 +32,27 @@ __device__ __forceinline__ float exp2_of(double x)
 // One block per (chunk slot, 32 heads).
 __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *delta, int64_t stride,
                                                          const float *A, const float *bias,
-                                                         int softplus, bool backward, float *tab)
+                                                         int softplus, bool backward, float *tab,
+                                                         Plan plan, int64_t *span)
 {
     __shared__ float sd[kC][33];
     const int64_t slot = blockIdx.x;
     const int h0 = blockIdx.y * 32, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (plan.mode == Plan::kAsk && blockIdx.x + blockIdx.y == 0) {
+        // the walks are cut only if the longest sequence would outlast two passes of pieces
+        __shared__ int longest;
+        if (tid == 0) longest = 0;
+        __syncthreads();
+        int most = 0;
+        for (int64_t s = tid; s < z.S; s += 256) {
+            int64_t lo, hi;
+            seq_bounds(z.cu, z.S, z.tok, s, lo, hi);
+            most = max(most, (int)((hi - lo + kC - 1) / kC));
+        }
+        atomicMax(&longest, most);
+        __syncthreads();
+        if (tid == 0) *span = longest > plan.limit ? plan.span : kNoSpan;
+    }
     const ChunkRef ck = find_chunk(z.cu, z.S, z.tok, kC, slot);
     if (ck.len == 0) return;
     const int h = h0 + lane;
@@ -78,15 +94,20 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
         for (int j = 0; j < 4; ++j) {
             const double c = pre + run[j];
             lv[j] = (float)(c - r);
-            ll[j] = (float)(c - r - (double)lv[j]);
             ev[j] = exp2_of(c);
             wn[j] = exp2_of(last - c);
             wv[j] = dv[j] * wn[j];
-            el[j] = exp2_of(c - r);
-            const float f = backward ? 1.0f : dv[j];
-            c1[j] = f * exp2_of(r1 - c);
-            c2[j] = f * exp2_of(r2 - c);
-            c3[j] = f * exp2_of(r3 - c);
+            if (backward) {
+                ll[j] = (float)(c - r - (double)lv[j]);
+                el[j] = exp2_of(c - r);
+                c1[j] = exp2_of(r1 - c);
+                c2[j] = exp2_of(r2 - c);
+                c3[j] = exp2_of(r3 - c);
+            } else {  // factors of M, which is rounded to bf16
+                c1[j] = dv[j] * ex2_approx((float)(r1 - c));
+                c2[j] = dv[j] * ex2_approx((float)(r2 - c));
+                c3[j] = dv[j] * ex2_approx((float)(r3 - c));
+            }
         }
         float *q = tab + (slot * z.H + h0 + i) * kTab;
         auto put = [&](int at, const float (&v)[4]) {
@@ -151,8 +172,9 @@ constexpr int state_smem()
 //              memory cost it 384 KB of traffic a chunk, 3000 clocks, against 192 KB.)
 //   issuer     multiplies into one of two tensor-memory buffers
 //   state      keep the state in registers, write it before each chunk, add the product
-// `segment` 0: whole sequences; 1: first pass of a split walk (from zero, only the end
-// state); 2: second pass (from the start states that head_join_kernel made).
+// A walk may be cut into segments that run side by side, in two passes: `first` makes every
+// segment's end state from zero (but the walk's last one's), then each segment starts from
+// the ones before it, joined in order: S = decay S + end.
 template <int NPAD, bool REV, int PLANES, bool VEC>
 __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, const __grid_constant__ CUtensorMap xmap,
                                                                    const __grid_constant__ CUtensorMap bmap)
@@ -167,16 +189,19 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     const Dims &z = a.z;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     // whole sequences go longest first: a long one started last would run almost alone
-    const int64_t slot = a.order ? a.order[blockIdx.y] : blockIdx.y;
+    const int64_t slot = a.order ? a.order[blockIdx.y] : blockIdx.y, span = a.asked ? *a.asked : a.span;
     const int per_group = (z.npan + 1) / 2;
     const int g = blockIdx.x / per_group, pan0 = blockIdx.x % per_group * 2;
     const int np = min(2, z.npan - pan0);  // panels of this CTA
-    const ChunkRef sg = find_chunk(z.cu, z.S, z.tok, a.span, slot);
-    if (sg.len == 0 && (sg.k != 0 || a.segment != 0)) return;
+    const ChunkRef sg = find_chunk(z.cu, z.S, z.tok, span, slot);
+    if (sg.len == 0 && sg.k != 0) return;
     const int nchunk = (sg.len + kC - 1) / kC;
     int64_t lo, hi;
     seq_bounds(z.cu, z.S, z.tok, sg.seq, lo, hi);
-    const int64_t first = lo / kC + sg.seq + (int64_t)sg.k * (a.span / kC);  // first chunk's slot
+    const int64_t first = lo / kC + sg.seq + (int64_t)sg.k * (span / kC);  // first chunk's slot
+    const int nseg = max(1, (int)((hi - lo + span - 1) / span));
+    const int before = REV ? nseg - 1 - sg.k : sg.k;  // segments walked before this one
+    if (a.first && before == nseg - 1) return;
 
     const uint32_t stages = (saddr(raw) + 1023) & ~1023u;
     if (tid == 0) {
@@ -340,30 +365,34 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
         const float *dec = a.tab + (c0 * z.H + sp.h) * kTab + kTabEc + kC - 1;
         const int64_t dec_step = dir * z.H * kTab;
 
+        auto seg_at = [&](int64_t sl) {
+            return reinterpret_cast<float4 *>(a.seg + (sl * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
+        };
         float st[COLS];
         {
             const float *src = nullptr;
-            if (a.segment == 0 && a.init && row_in)
+            if (!a.first && a.init && row_in)
                 src = a.init + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
-            const float4 *sgp = nullptr;
-            if (a.segment == 2 && has_s)
-                sgp = reinterpret_cast<const float4 *>(
-                          a.seg + (slot * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
 #pragma unroll
-            for (int i = 0; i < COLS / 4; ++i) {
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (sgp) v = sgp[i * 64];
-                st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
-                if (src)
+            for (int i = 0; i < COLS; ++i) st[i] = src && n0 + i < z.N ? src[n0 + i] : 0.0f;
+            for (int j = 0; j < (a.first ? 0 : before) && has_s; ++j) {
+                const int64_t other = slot - sg.k + (REV ? nseg - 1 - j : j);
+                const float4 *q = seg_at(other);
+                const float d = a.segdec[other * z.H + sp.h];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n0 + 4 * i + e < z.N) st[4 * i + e] = src[n0 + 4 * i + e];
+                for (int i = 0; i < COLS / 4; ++i) {
+                    const float4 v = q[i * 64];
+                    st[4 * i] = fmaf(d, st[4 * i], v.x);
+                    st[4 * i + 1] = fmaf(d, st[4 * i + 1], v.y);
+                    st[4 * i + 2] = fmaf(d, st[4 * i + 2], v.z);
+                    st[4 * i + 3] = fmaf(d, st[4 * i + 3], v.w);
+                }
             }
         }
         uint4 *mk = reinterpret_cast<uint4 *>(
                         a.marks + (c0 * z.G * z.npan + g * z.npan + si) * PLANES * kMark<NPAD>) + (n0 / 8) * 64 + p;
         const int64_t mk_step = dir * z.G * z.npan * PLANES * kMark<NPAD> / 8;
-        const bool marking = a.segment != 1 && has_s;
+        const bool marking = !a.first && has_s;
         float e = nchunk > 0 ? *dec : 1.0f;
         for (int kk = 0; kk < nchunk; ++kk) {
             if (marking) {
@@ -406,7 +435,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
             __syncwarp();
             if (lane == 0) mbar_arrive(&taken[kk & 1]);
         }
-        if (a.segment == 0 && a.final_ && row_in) {
+        if (!a.first && before == nseg - 1 && a.final_ && row_in) {
             float *dst = a.final_ + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
             const bool v4 = z.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.final_) % 16 == 0;
 #pragma unroll
@@ -421,9 +450,8 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
                         if (n + x < z.N) dst[n + x] = st[4 * i + x];
             }
         }
-        if (a.segment == 1 && has_s) {
-            float4 *q = reinterpret_cast<float4 *>(
-                            a.seg + (slot * z.G * z.npan + g * z.npan + si) * 64 * NPAD) + (n0 / 4) * 64 + p;
+        if (a.first && has_s) {
+            float4 *q = seg_at(slot);
 #pragma unroll
             for (int i = 0; i < COLS / 4; ++i)
                 q[i * 64] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
@@ -437,44 +465,6 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     umma::fence_before();
     __syncthreads();
     if (warp == 0) umma::dealloc(tm, 512);
-}
-
-// One block per (sequence, panel): turns the segments' end states from zero into their
-// start states, and leaves the sequence's final state.
-template <int NPAD, bool REV>
-__global__ void __launch_bounds__(256) head_join_kernel(StateArgs a)
-{
-    const Dims &z = a.z;
-    const int64_t s = blockIdx.x;
-    const int g = blockIdx.y / z.npan, pi = blockIdx.y % z.npan;
-    const PanelRef pr = panel_of(z, g, pi);
-    int64_t lo, hi;
-    seq_bounds(z.cu, z.S, z.tok, s, lo, hi);
-    const int nseg = (int)((hi - lo + a.span - 1) / a.span);
-    const int64_t base = lo / a.span + s;
-    for (int x = threadIdx.x; x < 16 * NPAD; x += 256) {
-        const int n = x / 64 * 4, p = x % 64;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float *e = &v.x;
-        const int64_t at = ((s * z.H + pr.h) * z.P + pr.p0 + p) * z.N + n;
-        if (a.init && p < pr.rows)
-            for (int i = 0; i < 4; ++i)
-                if (n + i < z.N) e[i] = a.init[at + i];
-        for (int k = 0; k < nseg; ++k) {
-            const int64_t slot = base + (REV ? nseg - 1 - k : k);
-            float4 *q = reinterpret_cast<float4 *>(a.seg + (slot * z.G * z.npan + g * z.npan + pi) * 64 * NPAD) + x;
-            const float4 end = *q;
-            const float dec = a.segdec[slot * z.H + pr.h];
-            *q = v;
-            v.x = fmaf(dec, v.x, end.x);
-            v.y = fmaf(dec, v.y, end.y);
-            v.z = fmaf(dec, v.z, end.z);
-            v.w = fmaf(dec, v.w, end.w);
-        }
-        if (a.final_ && p < pr.rows)
-            for (int i = 0; i < 4; ++i)
-                if (n + i < z.N) a.final_[at + i] = e[i];
-    }
 }
 
 template <int NPAD, bool REV, int PLANES, bool VEC>
@@ -498,24 +488,23 @@ cudaError_t launch_walk(const StateArgs &a, cudaStream_t st, int *launches)
 }
 
 template <int NPAD, bool REV, int PLANES>
-cudaError_t states(StateArgs a, bool split, bool vec, cudaStream_t st, int *launches)
+cudaError_t states(StateArgs a, const Plan &plan, bool vec, cudaStream_t st, int *launches)
 {
-    auto walk = [&](int segment) {
-        a.segment = segment;
+    auto walk = [&](bool first) {
+        a.first = first;
         return vec ? launch_walk<NPAD, REV, PLANES, true>(a, st, launches)
                    : launch_walk<NPAD, REV, PLANES, false>(a, st, launches);
     };
-    if (split) a.order = nullptr;
-    else if (a.order) {
+    a.span = plan.mode == Plan::kWhole ? kNoSpan : plan.span;
+    if (plan.mode != Plan::kAsk) a.asked = nullptr;
+    if (plan.mode != Plan::kWhole) {
+        a.order = nullptr;
+        if (cudaError_t e = walk(true); e != cudaSuccess) return e;
+    } else if (a.order) {
         if (cudaError_t e = launch_seq_order(a.z.cu, a.z.S, a.z.tok, a.order, st); e != cudaSuccess) return e;
         ++*launches;
     }
-    if (!split) return walk(0);
-    if (cudaError_t e = walk(1); e != cudaSuccess) return e;
-    head_join_kernel<NPAD, REV><<<dim3((unsigned)a.z.S, (unsigned)(a.z.G * a.z.npan)), 256, 0, st>>>(a);
-    ++*launches;
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    return walk(2);
+    return walk(false);
 }
 
 }  // namespace
@@ -535,46 +524,54 @@ Dims dims_of(const HeadScanArgs &a)
     return z;
 }
 
-// A split walk reads its inputs twice, so it pays once it more than doubles the CTAs at
-// work: below a third of the SMs.
-int64_t segment_span(const Dims &z, bool *split)
+// A cut walk reads its inputs twice, so with W chunks for every SM it takes about 2 W, one
+// that is not takes as long as the longest sequence. 8 x 12 walks (H = 24) of 134 chunks,
+// measured: the longest 54, 124 us whole and 85 us cut at 11; all of 16, 45 us whole and
+// 8 us more for the first pass that finds nothing to do. Where the lengths are only known on the device, the table kernel decides.
+Plan plan_of(const Dims &z, bool known)
 {
-    const int64_t walks = z.S * z.G * ((z.npan + 1) / 2);
-    const int64_t chunks = (z.tok + kC - 1) / kC;
-    *split = false;
-    if (walks * 3 > 148 || chunks < 8 * z.S) return (int64_t)1 << 31;
-    int64_t seg = (chunks * walks / z.S + 147) / 148;  // chunks a segment, for at most one CTA an SM
-    if (seg < 2) seg = 2;
-    *split = true;
-    return seg * kC;
+    Plan p;
+    const int64_t walks = z.G * ((z.npan + 1) / 2);  // of one sequence
+    const int64_t longest = (z.tok / z.S + kC - 1) / kC;
+    const int64_t chunks = known ? longest * z.S : z.tok / kC + z.S;
+    const int64_t load = (chunks * walks + 147) / 148;
+    p.limit = (int)(load * 11 / 5 + 4);
+    p.span = (load < 4 ? 4 : load) * kC;
+    if (known) p.mode = longest > p.limit ? Plan::kCut : Plan::kWhole;
+    // with two walks an SM the longest sequence first does as well; and no sequence is
+    // longer than all chunks together
+    else p.mode = walks * z.S >= 2 * 148 || z.tok / kC + 1 <= p.limit ? Plan::kWhole : Plan::kAsk;
+    return p;
 }
 
 cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, bool backward,
-                          cudaStream_t stream, int *launches)
+                          const Plan &plan, int64_t *span, cudaStream_t stream, int *launches)
 {
     const dim3 grid((unsigned)head_slots(z.tok, z.S, kC), (unsigned)((z.H + 31) / 32));
     head_table_kernel<<<grid, 256, 0, stream>>>(z, static_cast<const bf16 *>(a.delta), a.delta_stride,
-                                                a.A, a.dt_bias, a.delta_softplus, backward, tab);
+                                                a.A, a.dt_bias, a.delta_softplus, backward, tab,
+                                                plan, span);
     ++*launches;
     return cudaGetLastError();
 }
 
-cudaError_t launch_states(const StateArgs &a, bool rev, int planes, bool split, bool vec,
+cudaError_t launch_states(const StateArgs &a, bool rev, int planes, const Plan &plan, bool vec,
                           cudaStream_t st, int *launches)
 {
     const bool wide = a.z.N > 64;
     if (planes == 1)
-        return wide ? states<128, false, 1>(a, split, vec, st, launches)
-                    : states<64, false, 1>(a, split, vec, st, launches);
-    if (rev) return wide ? states<128, true, 2>(a, split, vec, st, launches)
-                         : states<64, true, 2>(a, split, vec, st, launches);
-    return wide ? states<128, false, 2>(a, split, vec, st, launches)
-                : states<64, false, 2>(a, split, vec, st, launches);
+        return wide ? states<128, false, 1>(a, plan, vec, st, launches)
+                    : states<64, false, 1>(a, plan, vec, st, launches);
+    if (rev) return wide ? states<128, true, 2>(a, plan, vec, st, launches)
+                         : states<64, true, 2>(a, plan, vec, st, launches);
+    return wide ? states<128, false, 2>(a, plan, vec, st, launches)
+                : states<64, false, 2>(a, plan, vec, st, launches);
 }
 
-Layout layout_of(const Dims &z, int planes, int64_t span, bool split)
+Layout layout_of(const Dims &z, int planes, const Plan &plan)
 {
-    const int64_t slots = head_slots(z.tok, z.S, kC), segs = split ? head_slots(z.tok, z.S, span) : 0;
+    const int64_t slots = head_slots(z.tok, z.S, kC);
+    const int64_t segs = plan.mode == Plan::kWhole ? 0 : head_slots(z.tok, z.S, plan.span);
     const int npad = z.N > 64 ? 128 : 64;
     const size_t panel = (size_t)z.G * z.npan * 64 * npad;
     Layout l;
@@ -583,7 +580,8 @@ Layout layout_of(const Dims &z, int planes, int64_t span, bool split)
     l.segdec = l.seg + up256((size_t)segs * panel * 4);
     l.marks = l.segdec + up256((size_t)segs * z.H * 4);
     l.order = l.marks + up256((size_t)slots * panel * 2 * planes);
-    l.total = l.order + up256(z.S > 1 ? (size_t)z.S * 4 : 0);
+    l.span = l.order + up256(z.S > 1 ? (size_t)z.S * 4 : 0);
+    l.total = l.span + 256;
     return l;
 }
 

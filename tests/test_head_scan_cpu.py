@@ -231,3 +231,52 @@ def test_written_out_gradients_match_autograd_and_differences(sp):
         diff = (loss({**t, k: v + e * step}) - loss({**t, k: v - e * step})) / (2 * e)
         want = (got[names[k]] * step).sum()
         assert abs(diff - want) <= 1e-6 * max(1.0, abs(want)), k
+
+
+def _plan(tok, H, P, G, S, known):
+    """How the bf16 kernels walk the sequences: ("whole", None), or ("cut" / "ask", tokens a segment)."""
+    npan = H // G * -(-P // 64)
+    walks = G * -(-npan // 2)
+    longest = -(-(tok // S) // 128)
+    chunks = longest * S if known else tok // 128 + S
+    load = (chunks * walks + 147) // 148
+    limit, span = load * 11 // 5 + 4, max(load, 4) * 128
+    if known:
+        return ("cut", span) if longest > limit else ("whole", None)
+    return ("whole", None) if walks * S >= 296 or tok // 128 + 1 <= limit else ("ask", span)
+
+
+def _up(n):
+    return -(-n // 256) * 256
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_workspaces_hold_dense_and_packed_walks(bwd):
+    """The size is asked for without cu_seqlens, so it covers the tables, the segments' states,
+    the marks and the rest of either kind of call, whichever needs more."""
+    rng = np.random.default_rng(1)
+    cases = [(270336, 2, 64, 1, 64, 3), (270336, 128, 64, 2, 64, 3), (16384, 24, 64, 1, 128, 8), (8192, 128, 64, 8, 128, 1),
+             (5000, 2, 64, 1, 128, 1), (6000, 2, 64, 1, 128, 2), (0, 2, 64, 1, 64, 2), (1, 1, 1, 1, 1, 1)]
+    for _ in range(300):
+        G = int(rng.choice([1, 2, 8]))
+        cases.append((int(np.exp(rng.uniform(0, 13))), G * int(rng.integers(1, 20)), int(rng.integers(1, 257)), G,
+                      int(rng.integers(1, 129)), int(rng.integers(1, 60))))
+    packed_larger = 0
+    for tok, H, P, G, N, S in cases:
+        size = (ssm.ssm_head_scan_bwd_workspace_size if bwd else ssm.ssm_head_scan_workspace_size)(
+            tok, H, P, G, N, S, torch.bfloat16)
+        slots, np_ = tok // 128 + S, -(-P // 64)
+        panel = H * np_ * 64 * (128 if N > 64 else 64)
+        need = []
+        for known in (True, False):
+            mode, span = _plan(tok, H, P, G, S, known)
+            segs = 0 if mode == "whole" else tok // span + S
+            marks = _up(slots * panel * 2 * (2 if bwd else 1))
+            n = _up(slots * H * (7 * 128 + 192) * 4) + _up(segs * panel * 4) + _up(segs * H * 4) + marks
+            n += _up(4 * S if S > 1 else 0) + 256
+            if bwd:  # the gradients' marks, at least one range of dG tiles, the chunks' shares
+                n += marks + _up(slots * G * 128 * 128 * 4) + _up(slots * H * 12)
+            need.append(n)
+        assert size >= max(need), (tok, H, P, G, N, S, size, need)
+        packed_larger += need[1] > need[0]
+    assert packed_larger  # the case that a size from the dense plan alone would miss
