@@ -62,56 +62,91 @@ __device__ __forceinline__ float2 team_sum(float2 v, float2 (*sm)[32], int turn)
     return v;
 }
 
+// V elements as 32-bit words, moved 16 (or 8) bytes at a time.
+template <typename E, int V>
+struct Raw {
+    static constexpr int W = V * sizeof(E) / 4;
+    uint32_t w[W];
+    template <typename F>
+    __device__ __forceinline__ void load(const E *p, F get)
+    {
+        if constexpr (W == 2) {
+            const uint2 v = get(reinterpret_cast<const uint2 *>(p));
+            w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 v = get(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(const E *p)
+    {
+        load(p, [](auto q) { return __ldcs(q); });  // read once
+    }
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        if (sizeof(E) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
+
 template <typename T, int V>
 __device__ __forceinline__ void load_f(const T *p, float (&v)[V])
 {
-    if constexpr (V * sizeof(T) == 32) {
-        float a[V / 2], b[V / 2];
-        load_vec<T, V / 2>(p, a);
-        load_vec<T, V / 2>(p + V / 2, b);
+    Raw<T, V> r;
+    r.load(p, [](auto q) { return __ldg(q); });
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) { v[i] = a[i]; v[V / 2 + i] = b[i]; }
-    } else {
-        load_vec<T, V>(p, v);
-    }
+    for (int i = 0; i < V; ++i) v[i] = r[i];
 }
 
 // read-write data (a residual stream updated in place): no read-only cache
 template <typename T, int V>
 __device__ __forceinline__ void load_rw(const T *p, float (&v)[V])
 {
-    static_assert((V * sizeof(T)) % 16 == 0, "16-byte vectors");
+    Raw<T, V> r;
+    r.load(p, [](auto q) { return *q; });
 #pragma unroll
-    for (int q = 0; q < (int)(V * sizeof(T) / 16); ++q) {
-        const uint4 raw = reinterpret_cast<const uint4 *>(p)[q];
-        const T *e = reinterpret_cast<const T *>(&raw);
-#pragma unroll
-        for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[q * (16 / sizeof(T)) + i] = to_f32(e[i]);
-    }
+    for (int i = 0; i < V; ++i) v[i] = r[i];
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 template <typename T, int V>
 __device__ __forceinline__ void store_f(T *p, const float (&v)[V])
 {
-    if constexpr (V * sizeof(T) == 32) {
-        float a[V / 2], b[V / 2];
+    constexpr int W = V * sizeof(T) / 4;
+    uint32_t w[W];
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) { a[i] = v[i]; b[i] = v[V / 2 + i]; }
-        store_vec<T, V / 2>(p, a);
-        store_vec<T, V / 2>(p + V / 2, b);
+    for (int i = 0; i < W; ++i) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+        else w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (W == 2) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     } else {
-        store_vec<T, V>(p, v);
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
 }
 
-// V elements per vector: 8 for bf16 activations, 4 for fp32.
-template <typename T> struct VecOf { static constexpr int v = 16 / sizeof(T); };
+// Elements per vector: 16 bytes of the widest tensor of a row. Beside an fp32 stream bf16
+// goes 8 bytes at a time: two 16-byte halves of fp32 32 bytes apart cost twice the
+// cache's time.
+template <typename T, typename R> struct VecOf { static constexpr int v = sizeof(T) == 2 && sizeof(R) == 2 ? 8 : 4; };
 
 // MODE 0: x only; 1: gate then norm; 2: norm then gate; 3: residual.
 template <typename T, typename R, int MODE, bool WARP, int K>
 __global__ void __launch_bounds__(WARP ? 256 : 512) norm_fwd_kernel(Args a)
 {
-    constexpr int V = VecOf<T>::v;
+    constexpr int V = VecOf<T, R>::v;
     __shared__ float2 sm[2][32];
     const int TEAM = WARP ? 32 : blockDim.x;
     const int l = WARP ? threadIdx.x % 32 : threadIdx.x;
@@ -175,26 +210,11 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) norm_fwd_kernel(Args a)
     }
 }
 
-// A vector's worth of one tensor as loaded: V elements of E.
-template <typename E, int V>
-struct Raw {
-    uint4 q[V * sizeof(E) / 16];
-    __device__ __forceinline__ void load(const E *p)
-    {
-#pragma unroll
-        for (int i = 0; i < (int)(V * sizeof(E) / 16); ++i) q[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-    }
-    __device__ __forceinline__ float operator[](int i) const
-    {
-        return to_f32(reinterpret_cast<const E *>(q)[i]);
-    }
-};
-
 // Teams walk rows with a stride; thread l keeps the weight-gradient sums of its columns.
 template <typename T, typename R, int MODE, bool WARP, int K, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
 {
-    constexpr int V = VecOf<T>::v;
+    constexpr int V = VecOf<T, R>::v;
     __shared__ float2 sm[2][32];
     const int TEAM = WARP ? 32 : blockDim.x;
     const int l = WARP ? threadIdx.x % 32 : threadIdx.x;
@@ -203,32 +223,30 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
     const int gs = a.group, c0 = blockIdx.y * gs;
     struct Row {
         Raw<T, V> x, dy;                     // x of MODE 3 only for its scale's gradient
-        Raw<T, MODE == 1 || MODE == 2 ? V : 16 / sizeof(T)> z;
+        Raw<T, V> z;
         Raw<R, V> r, g;                      // MODE 3: the stream and its incoming gradient
     };
     Row cur[K];
-    auto load = [&](int64_t row, Row (&to)[K]) {
-        if (row >= a.tok) return;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (l + TEAM * k) * V;
-            if (c >= gs) continue;
-            const int64_t at = row * a.D + c0 + c;
-            to[k].dy.load(static_cast<const T *>(a.dy) + at);
-            if (MODE != 3 || a.has_ds) to[k].x.load(static_cast<const T *>(a.x) + row * a.xs + c0 + c);
-            if (MODE == 1 || MODE == 2) to[k].z.load(static_cast<const T *>(a.z) + row * a.zs + c0 + c);
-            if (MODE == 3) {
-                to[k].r.load(static_cast<const R *>(a.xres) + at);
-                if (a.dro) to[k].g.load(static_cast<const R *>(a.dro) + at);
-            }
+    auto load = [&](int64_t row, int k, Row &to) {
+        const int c = (l + TEAM * k) * V;
+        if (row >= a.tok || c >= gs) return;
+        const int64_t at = row * a.D + c0 + c;
+        to.dy.load(static_cast<const T *>(a.dy) + at);
+        if (MODE != 3 || a.has_ds) to.x.load(static_cast<const T *>(a.x) + row * a.xs + c0 + c);
+        if (MODE == 1 || MODE == 2) to.z.load(static_cast<const T *>(a.z) + row * a.zs + c0 + c);
+        if (MODE == 3) {
+            to.r.load(static_cast<const R *>(a.xres) + at);
+            if (a.dro) to.g.load(static_cast<const R *>(a.dro) + at);
         }
     };
     float dw[K][V] = {}, ds[MODE == 3 ? K : 1][V] = {};
-    load(team, cur);
+#pragma unroll
+    for (int k = 0; k < K; ++k) load(team, k, cur[k]);
     int turn = 0;
     for (int64_t row = team; row < a.tok; row += teams, ++turn) {
         Row next[K];
-        load(row + teams, next);
+#pragma unroll
+        for (int k = 0; k < K; ++k) load(row + teams, k, next[k]);
         float ss = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -446,7 +464,7 @@ unsigned block_of(int nv, int K) { return (unsigned)(((nv + K - 1) / K + 31) / 3
 template <typename T, typename R, int MODE>
 cudaError_t fwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st)
 {
-    constexpr int V = VecOf<T>::v;
+    constexpr int V = VecOf<T, R>::v;
     const unsigned groups = (unsigned)(n.D / n.group);
     const int nv = (int)(n.group / V);
     const dim3 warps((unsigned)((n.tok + 7) / 8), groups), rows((unsigned)n.tok, groups);
@@ -472,7 +490,7 @@ int resident(const void *kernel, int threads)
 template <typename T, typename R, int MODE>
 cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int *parts)
 {
-    constexpr int V = VecOf<T>::v;
+    constexpr int V = VecOf<T, R>::v;
     const int64_t groups = n.D / n.group;
     const int nv = (int)(n.group / V);
     const bool warp = vec && nv <= 64;
@@ -556,7 +574,7 @@ cudaError_t launch_norm_fwd(const NormArgs &n, cudaStream_t st, int *launches)
     return by_type(n, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const bool vec = vectors(n, VecOf<T>::v);
+        const bool vec = vectors(n, VecOf<T, R>::v);
         if (!n.gated) return fwd<T, R, 3>(n, a, vec, st);
         if (!n.z) return fwd<T, R, 0>(n, a, vec, st);
         return n.norm_before_gate ? fwd<T, R, 2>(n, a, vec, st) : fwd<T, R, 1>(n, a, vec, st);
@@ -572,7 +590,7 @@ cudaError_t launch_norm_bwd(const NormArgs &n, cudaStream_t st, int *launches)
         const cudaError_t e = by_type(n, [&](auto t, auto r) {
             using T = decltype(t);
             using R = decltype(r);
-            const bool vec = vectors(n, VecOf<T>::v);
+            const bool vec = vectors(n, VecOf<T, R>::v);
             if (!n.gated) return bwd<T, R, 3>(n, a, vec, st, &parts);
             if (!n.z) return bwd<T, R, 0>(n, a, vec, st, &parts);
             return n.norm_before_gate ? bwd<T, R, 2>(n, a, vec, st, &parts)
