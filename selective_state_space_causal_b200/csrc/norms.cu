@@ -7,13 +7,21 @@
 // Backward, with vh = v rstd, dh = dy w (times the gate when it comes after the norm):
 //   dv = rstd (dh - vh mean(dh vh)),  dw = sum over rows of dy vh (times the gate).
 //
-// All four are bound by memory: every input is read once and every output written
+// All four move each byte once: every input is read once and every output written
 // once, because a team of threads (a warp for groups up to 64 vectors, a block sized to
 // the row beyond) keeps its row in registers between the sums and the scaling. The
 // backward keeps the row as it was loaded, computes from it twice, and loads the next
-// row before it waits for this one's sums. Vectors are 16 bytes of activations. Rows
-// that are not 16-byte aligned, or longer than the registers hold, go to kernels that
-// read the row twice (the second time from cache).
+// row before it waits for this one's sums; the weights and their gradients' sums stay in
+// registers over all rows of a block (weights read per row: 244 us for the first line
+// below). Rows that are not 16-byte aligned, or longer than the registers hold, go to
+// kernels that read the row twice (the second time from cache).
+//
+// Measured on a B200, bf16, 16384 rows, of a copy's 6534 GB/s:
+//   gate then norm, 5120 wide      forward 100 us (5.0 TB/s, 77%), backward 232 us (3.6 TB/s, 55%)
+//   residual in fp32, 2560 wide    forward  79 us (6.4 TB/s, 97%), backward 152 us (4.4 TB/s, 67%)
+// The forward with a gate and both backwards are held by what a row waits for: its loads,
+// one sum over the block, its stores, with 20 warps an SM in flight (registers), and by
+// the exponentials and reciprocals of the gate, taken twice an element in the backward.
 #include "common.cuh"
 #include "internal.h"
 
@@ -242,6 +250,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
     float dw[K][V] = {}, ds[MODE == 3 ? K : 1][V] = {};
 #pragma unroll
     for (int k = 0; k < K; ++k) load(team, k, cur[k]);
+    float weight[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (l + TEAM * k) * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) weight[k][i] = 1.0f;
+        if (a.w && c < gs) load_f<float, V>(a.w + c0 + c, weight[k]);
+    }
     int turn = 0;
     for (int64_t row = team; row < a.tok; row += teams, ++turn) {
         Row next[K];
@@ -252,8 +268,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
         for (int k = 0; k < K; ++k) {
             const int c = (l + TEAM * k) * V;
             if (c >= gs) continue;
-            float wv[V];
-            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
+            const float (&wv)[V] = weight[k];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float v = MODE == 3 ? cur[k].r[i] : cur[k].x[i], q = cur[k].dy[i];
@@ -263,7 +278,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
                     else q *= gv;
                 }
                 ss = fmaf(v, v, ss);
-                dot = fmaf(a.w ? q * wv[i] : q, v, dot);
+                dot = fmaf(q * wv[i], v, dot);
             }
         }
         const float2 both = team_sum<WARP>(make_float2(ss, dot), sm, turn);
@@ -274,11 +289,10 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(Args a)
             const int c = (l + TEAM * k) * V;
             if (c >= gs) continue;
             const int64_t at = row * a.D + c0 + c;
-            float wv[V], o1[V], o2[V];
-            if (a.w) load_f<float, V>(a.w + c0 + c, wv);
+            float o1[V], o2[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float w = a.w ? wv[i] : 1.0f, yv = cur[k].dy[i];
+                const float w = weight[k][i], yv = cur[k].dy[i];
                 if (MODE == 0) {
                     const float v = cur[k].x[i];
                     dw[k][i] = fmaf(yv, v * rstd, dw[k][i]);
@@ -438,9 +452,12 @@ __global__ void __launch_bounds__(256) norm_bwd_any_kernel(Args a)
     }
 }
 
-// out[c] = sum over partial rows, in a fixed order: 32 columns by 32 strides of rows a block.
-__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *part, int parts, int D, float *out)
+// Sums over partial rows, in a fixed order: 32 columns by 32 strides of rows a block.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *part, int parts, int D, float *dw, float *ds)
 {
+    if (blockIdx.y) part += (int64_t)parts * D;  // the second plane is the scale's
+    float *out = blockIdx.y ? ds : dw;
+    if (!out) return;
     __shared__ double sm[32][32];
     const int lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane, r0 = threadIdx.x / 32;
     double s = 0.0;
@@ -599,15 +616,11 @@ cudaError_t launch_norm_bwd(const NormArgs &n, cudaStream_t st, int *launches)
         if (e != cudaSuccess) return e;
     }
     const unsigned blocks = (unsigned)((n.D + 31) / 32);
-    float *outs[2] = {n.dweight, n.dscale};
-    for (int i = 0; i < 2; ++i) {
-        if (!outs[i]) continue;
-        norm_reduce_kernel<<<blocks, 1024, 0, st>>>(n.partials + (size_t)i * parts * n.D, parts,
-                                                   (int)n.D, outs[i]);
-        ++*launches;
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    if (!n.dweight && !n.dscale) return cudaSuccess;
+    norm_reduce_kernel<<<dim3(blocks, n.dscale ? 2 : 1), 1024, 0, st>>>(n.partials, parts, (int)n.D,
+                                                                       n.dweight, n.dscale);
+    ++*launches;
+    return cudaGetLastError();
 }
 
 }  // namespace ssm
