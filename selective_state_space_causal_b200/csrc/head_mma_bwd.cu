@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
         constexpr int DOTS = PLANE / 16;
         const int dot0 = (wi == 3 ? 0 : DOTS * 5 / 8) + cg * 32 + lane, dot1 = wi == 3 ? DOTS * 5 / 8 : DOTS;
         if (wi < 2 && lane == 0) sums[0].dot[warp] = sums[1].dot[warp] = 0.0f;
-        float dg[4][8];
+        float dg[4][8];  // of blocks wi, wi + 1 ..
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -406,13 +406,14 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
             const f32x2 d2 = pk2(ds, ds);
             f32x2 k2 = pk2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j < wi) continue;
+            for (int i = 0; i < 4; ++i) {
+                const int j = wi + i;  // counted from the diagonal: its code exists once
+                if (j > 3) break;
                 uint32_t gv[8], mv[8], w[4];
                 umma::ld8(kG + me + 32 * j + 8 * cg, gv);
                 umma::ld8(kDm + me + 32 * j + 8 * cg, mv);
                 float L[8];
-                if (j > wi) {
+                if (i > 0) {
                     const float rn = tb[col_at(j) + row];
                     const f32x2 r2 = pk2(rn, rn);
                     const float4 ea = *reinterpret_cast<const float4 *>(tb + kTabEl + 32 * j + 8 * cg);
@@ -440,13 +441,13 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
                     const f32x2 g2 = pk2(__uint_as_float(gv[c]), __uint_as_float(gv[c + 1]));
                     const f32x2 m2 = pk2(__uint_as_float(mv[c]), __uint_as_float(mv[c + 1]));
                     const f32x2 gl = mul2(g2, l2), xl = mul2(m2, l2);
-                    f32x2 acc = fma2(xl, d2, pk2(dg[j][c], dg[j][c + 1]));
-                    upk2(acc, dg[j][c], dg[j][c + 1]);
+                    f32x2 acc = fma2(xl, d2, pk2(dg[i][c], dg[i][c + 1]));
+                    upk2(acc, dg[i][c], dg[i][c + 1]);
                     float m0, m1, w0, w1;
                     upk2(mul2(gl, d2), m0, m1);
                     w[c / 2] = umma::pack(m0, m1);
                     f32x2 wl = mul2(m2, gl);
-                    if (j == wi) {  // the diagonal apart
+                    if (i == 0) {  // the diagonal apart
                         upk2(wl, w0, w1);
                         const bool q0 = 8 * cg + c == lane, q1 = 8 * cg + c + 1 == lane;
                         own = q0 ? w0 : q1 ? w1 : own;
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
         char *tile = reinterpret_cast<char *>(a.dg + ((slot * z.G + g) * a.ranges + range) * (int64_t)(2 * kC * kC));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int c = 4 * j + cg;
+            const int c = 4 * ((wi + j) & 3) + cg;  // blocks before the diagonal are zeros
             char *to = tile + (c / 8) * umma::kPanel + umma::piece(row, c % 8);
             uint32_t hi[4], lo[4];
 #pragma unroll
