@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    bool failed = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, failed, &g_bwd_status); };
+    unsigned tries = umma::kTries;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, tries, &g_bwd_status); };
     const int64_t mark0 = (slot * z.G * z.npan + g * z.npan + pb) * 2 * kMark<NPAD>;  // both planes of a panel
 
     if (warp == kBLoader) {
@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(kBcThreads) head_bwd_bc_kernel(BwdArgs a, cons
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    bool failed = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, failed, &g_bwd_status); };
+    unsigned tries = umma::kTries;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, tries, &g_bwd_status); };
 
     if (warp == kWork + 1) {  // loader
         for (int it = 0; it < count; ++it) {

@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(kOutThreads) head_out_kernel(OutArgs a, const 
     constexpr uint32_t tm = umma::kWhole;
     const uint32_t tM = tm + 128 + team * 192, tYa = tM + 64, tYb = tM + 128;
     const int p0 = pb + team, count = p0 < pe ? (pe - p0 + kTeams - 1) / kTeams : 0;
-    bool failed = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, failed, &g_out_status); };
+    unsigned tries = umma::kTries;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, tries, &g_out_status); };
 
     if (warp >= kOutLoader) {
         for (int it = 0; it < count + 2; ++it) {

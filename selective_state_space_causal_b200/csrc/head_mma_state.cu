@@ -224,10 +224,10 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     __syncthreads();
     umma::fence_after();
     constexpr uint32_t tm = umma::kWhole, planes = tm + 256;  // two products, then 4 x 3 planes of 16 columns
-    bool failed = false;
+    unsigned tries = umma::kTries;
     auto chunk_at = [&](int kk) { return REV ? nchunk - 1 - kk : kk; };
     auto len_of = [&](int k) { return min(kC, sg.len - k * kC); };
-    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, failed, &g_status); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { umma::wait(bar, parity & 1, tries, &g_status); };
 
     if (warp == kLoader) {
         const PanelRef q0 = panel_of(z, g, pan0), q1 = panel_of(z, g, pan0 + np - 1);

@@ -125,11 +125,14 @@ __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.
 
 // mbar_wait for barriers that matrix instructions complete: these waits are short and
 // on the critical path, so they poll with the hardware's own suspend time. At most 2^22
-// tries, then bit 1 of *status is set and this thread waits no more.
-__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &failed, int *status)
+// tries, then bit 1 of *status is set and each later wait of this thread tries once. The
+// count of tries is hidden from the compiler, which otherwise makes a second copy of
+// the code behind a wait for the case that it failed: the instruction cache feels it.
+constexpr unsigned kTries = 1u << 22;
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, unsigned &tries, int *status)
 {
-    if (failed) return;
-    for (unsigned i = 0; i < 1u << 22; ++i) {
+#pragma unroll 1
+    for (unsigned i = 0; i < tries; ++i) {
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
@@ -137,7 +140,7 @@ __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &faile
             : "=r"(done) : "r"(saddr(bar)), "r"(parity) : "memory");
         if (done) return;
     }
-    failed = true;
+    asm volatile("mov.u32 %0, 1;" : "=r"(tries));
     atomicOr(status, 1);
 }
 
