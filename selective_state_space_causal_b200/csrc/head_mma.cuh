@@ -92,7 +92,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t
     const bf16 *q = src + r0 * stride + 8 * c;
     const int64_t step = ROWS * stride;
     const uint32_t at = dst + (c / 8) * umma::kPanel;
-#pragma unroll
+#pragma unroll 8
     for (int i = 0; i < kC / ROWS; ++i) {
         const int r = r0 + ROWS * i;
         const bool in = r < len && n > 0;
