@@ -14,6 +14,12 @@
 // the exact bf16 inputs, V and Yi from two planes of the states (17 bits), and the sums
 // are fp32. Rounded to bf16 once: M as a left operand (of du), the states that dB and dC
 // take in from other chunks.
+//
+// Measured on a B200, 32768 tokens, 80 heads of 64 x 128: head_bwd_kernel 614 us (2.6 GB:
+// u, dy, du, four planes of states: 4.2 TB/s, 65% of a copy's rate; issue slots 60% used,
+// the matrix pipe 23%), head_bwd_bc_kernel 238 us (1.5 GB, 6.3 TB/s, 96%). The first is
+// bound by its 16 compute warps' instructions and their latency, and was held by the
+// instruction cache before: 119 KB of code took 860 us, 75 KB takes 614.
 #include <type_traits>
 
 #include "head_mma.cuh"

@@ -8,6 +8,14 @@
 // state keeps fp32 accuracy; b is bf16 as given. The products of different chunks are
 // independent: only S' = e S + delta runs chunk after chunk, in registers, while the
 // next products are under way.
+//
+// Measured on a B200, 80 heads of 64 x 128 in one group: 65536 tokens in 43 sequences, one
+// plane of marks, 369 us (1.34 GB of x, marks and tables: 3.6 TB/s, 56% of a copy's rate;
+// 24% of the matrix rate for the one product the mathematics needs in three planes);
+// 32768 tokens in 21 sequences, two planes, 258 us forward and 283 us reverse (1.06 GB, 4.1
+// TB/s). Bound by the converters' latency (below), not by memory: without the marks'
+// stores the last two would take 233 and 257 us, with a split that costs nothing 263 and
+// 278. Marks sent by bulk copies instead of the threads' own stores: 5% slower.
 #include <type_traits>
 
 #include "head_mma.cuh"
@@ -29,7 +37,9 @@ __device__ __forceinline__ float exp2_of(double x)
     return fmaf(r, (float)(x - (double)h) * 0.6931471806f, r);
 }
 
-// One block per (chunk slot, 32 heads).
+// One block per (chunk slot, 32 heads). Sums and their differences are 64-bit. Bound by
+// the latency of a block's few steps: 56 us for 65536 tokens of 80 heads (0.18 GB), 18 us
+// for 16384 of 24.
 __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *delta, int64_t stride,
                                                          const float *A, const float *bias,
                                                          int softplus, bool backward, float *tab,
@@ -162,14 +172,30 @@ constexpr int state_smem()
     return 1024 + kStages * state_stage<NPAD>();
 }
 
+// The segment behind a slot; whole sequences need no search.
+__device__ __forceinline__ ChunkRef segment_of(const Dims &z, int64_t span, int64_t slot)
+{
+    if (span <= z.tok) return find_chunk(z.cu, z.S, z.tok, span, slot);
+    ChunkRef r;
+    int64_t lo, hi;
+    r.seq = (int)min(slot, z.S - 1);
+    r.k = (int)(slot - r.seq);
+    seq_bounds(z.cu, z.S, z.tok, r.seq, lo, hi);
+    r.start = lo;
+    r.len = r.k == 0 ? (int)(hi - lo) : 0;
+    r.last = true;
+    return r;
+}
+
 // One CTA has two panels of one group and walks a segment's chunks. The warps have
 // roles, so that loads, conversion, matrix instructions and state updates of
 // neighbouring chunks run at the same time (with all warps in step, each phase's
 // latency was exposed: 5500 clocks a chunk against 1536 of matrix instructions):
 //   loader     copies x, b and weights of the next chunks into one of three stages
 //   converters make w x as three planes in tensor memory, transposed on the way, 32
-//              tokens at a time, three groups of four warps in turn. (Planes in shared
-//              memory cost it 384 KB of traffic a chunk, 3000 clocks, against 192 KB.)
+//              tokens at a time, three groups of four warps in turn: 2000 clocks a step,
+//              so 3000 a chunk; a fourth group does not fit in the registers. (Planes in
+//              shared memory cost it 384 KB of traffic a chunk against 192 KB.)
 //   issuer     multiplies into one of two tensor-memory buffers
 //   state      keep the state in registers, write it before each chunk, add the product
 // A walk may be cut into segments that run side by side, in two passes: `first` makes every
@@ -193,7 +219,7 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     const int per_group = (z.npan + 1) / 2;
     const int g = blockIdx.x / per_group, pan0 = blockIdx.x % per_group * 2;
     const int np = min(2, z.npan - pan0);  // panels of this CTA
-    const ChunkRef sg = find_chunk(z.cu, z.S, z.tok, span, slot);
+    const ChunkRef sg = segment_of(z, span, slot);
     if (sg.len == 0 && sg.k != 0) return;
     const int nchunk = (sg.len + kC - 1) / kC;
     int64_t lo, hi;
@@ -309,8 +335,14 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
             const float2 *w = reinterpret_cast<const float2 *>(
                 raw + (sb + BP * umma::kPanel + cp * 512 + q * 128 - saddr(raw))) + lane % 4;
             wait(&landed[st], kk / kStages);
-            if (kk > 0) wait(&eaten[q], kk - 1);
-            umma::fence_after();
+            // loads first: a wait takes some 250 clocks even if there is nothing to wait for
+            uint32_t x[2][8], v[3][8];
+#pragma unroll
+            for (int ph = 0; ph < 2; ++ph)  // 16 state rows
+#pragma unroll
+                for (int th = 0; th < 2; ++th)  // 16 tokens
+                    umma::ldsm_t(sx + cp * umma::kPanel + umma::piece(32 * q + 16 * th + tt, pc + 2 * ph),
+                                 x[ph][4 * th], x[ph][4 * th + 1], x[ph][4 * th + 2], x[ph][4 * th + 3]);
             f32x2 wt[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -325,23 +357,20 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
                 }
                 fence_proxy_async();
             }
+            if (kk > 0) wait(&eaten[q], kk - 1);
+            umma::fence_after();
 #pragma unroll
-            for (int ph = 0; ph < 2 && has_x; ++ph) {  // 16 state rows
-                uint32_t x[8], v[3][8];
-#pragma unroll
-                for (int th = 0; th < 2; ++th)  // 16 tokens
-                    umma::ldsm_t(sx + cp * umma::kPanel + umma::piece(32 * q + 16 * th + tt, pc + 2 * ph),
-                                 x[4 * th], x[4 * th + 1], x[4 * th + 2], x[4 * th + 3]);
+            for (int ph = 0; ph < 2 && has_x; ++ph) {
                 if (len < 32) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int t = 8 * (i / 2) + 2 * (lane % 4);
                         const uint32_t keep = (t < len ? 0xFFFFu : 0u) | (t + 1 < len ? 0xFFFF0000u : 0u);
-                        x[i] &= keep;
+                        x[ph][i] &= keep;
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split3(x[i], wt[i / 2], v[0][i], v[1][i], v[2][i]);
+                for (int i = 0; i < 8; ++i) split3(x[ph][i], wt[i / 2], v[0][i], v[1][i], v[2][i]);
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
                     umma::st_tiles(planes + rows + ((uint32_t)ph << 20) + (3 * q + s) * 16, v[s]);
