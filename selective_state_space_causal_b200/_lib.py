@@ -114,9 +114,7 @@ def _check(code: int) -> None:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
     return t.data_ptr()
 
@@ -403,6 +401,10 @@ class _NormScalars(ctypes.Structure):
 
 def _token_stride(t, what: str) -> int:
     """Elements between tokens of a (tok, ...) tensor whose tokens are contiguous rows."""
+    if t.is_contiguous():
+        n = t.shape[0]
+        if n:
+            return t.numel() // n
     shape, stride, width = t.shape, t.stride(), 1
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != width and shape[i] != 1:
@@ -464,10 +466,10 @@ def _on_gpu(*tensors) -> None:
         if t is None:
             continue
         d = t.get_device()  # -1: host memory
-        if here is None and d >= 0:
-            here = torch.cuda.current_device()
-        if d < 0 or d != here:
-            raise SsmError(-1, f"a tensor is on {t.device}, not on the current CUDA device")
+        if d != here:
+            if here is not None or d < 0 or d != torch.cuda.current_device():
+                raise SsmError(-1, f"a tensor is on {t.device}, not on the current CUDA device")
+            here = d
 
 
 def _bytes(t) -> int:

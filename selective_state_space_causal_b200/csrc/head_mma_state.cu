@@ -199,8 +199,9 @@ __device__ __forceinline__ ChunkRef segment_of(const Dims &z, int64_t span, int6
 //   issuer     multiplies into one of two tensor-memory buffers
 //   state      keep the state in registers, write it before each chunk, add the product
 // A walk may be cut into segments that run side by side, in two passes: `first` makes every
-// segment's end state from zero (but the walk's last one's), then each segment starts from
-// the ones before it, joined in order: S = decay S + end.
+// segment's end state from zero (but the walk's last one's) and a copy of the initial
+// state, then each segment starts from that and the ends before it, joined in order: S =
+// decay S + end.
 template <int NPAD, bool REV, int PLANES, bool VEC>
 __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, const __grid_constant__ CUtensorMap xmap,
                                                                    const __grid_constant__ CUtensorMap bmap)
@@ -227,7 +228,22 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
     const int64_t first = lo / kC + sg.seq + (int64_t)sg.k * (span / kC);  // first chunk's slot
     const int nseg = max(1, (int)((hi - lo + span - 1) / span));
     const int before = REV ? nseg - 1 - sg.k : sg.k;  // segments walked before this one
-    if (a.first && before == nseg - 1) return;
+    if (a.first && before == nseg - 1) {
+        // This segment's end is not asked for: its place keeps the walk's initial state,
+        // whose own memory `final_` may be, for all segments of the second pass.
+        const int entries = 64 * (NPAD / 4);
+        for (int i = tid; nseg > 1 && a.init && i < np * entries; i += kStateThreads) {
+            const int q = i / entries, n = i % entries / 64 * 4, p = i % 64;
+            const PanelRef sp = panel_of(z, g, pan0 + q);
+            const float *src = a.init + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = p < sp.rows && n + e < z.N ? src[n + e] : 0.0f;
+            reinterpret_cast<float4 *>(a.seg + (slot * z.G * z.npan + g * z.npan + pan0) * 64 * NPAD)[i] =
+                make_float4(v[0], v[1], v[2], v[3]);
+        }
+        return;
+    }
 
     const uint32_t stages = (saddr(raw) + 1023) & ~1023u;
     if (tid == 0) {
@@ -400,10 +416,18 @@ __global__ void __launch_bounds__(kStateThreads) head_state_kernel(StateArgs a, 
         float st[COLS];
         {
             const float *src = nullptr;
-            if (!a.first && a.init && row_in)
+            if (!a.first && a.init && row_in && nseg == 1)
                 src = a.init + (((int64_t)sg.seq * z.H + sp.h) * z.P + sp.p0 + p) * z.N;
 #pragma unroll
             for (int i = 0; i < COLS; ++i) st[i] = src && n0 + i < z.N ? src[n0 + i] : 0.0f;
+            if (!a.first && a.init && has_s && nseg > 1) {
+                const float4 *q = seg_at(slot - sg.k + (REV ? 0 : nseg - 1));
+#pragma unroll
+                for (int i = 0; i < COLS / 4; ++i) {
+                    const float4 v = q[i * 64];
+                    st[4 * i] = v.x; st[4 * i + 1] = v.y; st[4 * i + 2] = v.z; st[4 * i + 3] = v.w;
+                }
+            }
             for (int j = 0; j < (a.first ? 0 : before) && has_s; ++j) {
                 const int64_t other = slot - sg.k + (REV ? nseg - 1 - j : j);
                 const float4 *q = seg_at(other);

@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(128) head_recurrent_kernel(RecArgs a)
     __shared__ __align__(16) float sB[kQ][NP], sC[kQ][NP];
     __shared__ float sx[kQ][kPT + 1], sa[kQ], sd[kQ];
     const int tid = threadIdx.x, j = tid % LR, pr = tid / LR;
-    const int64_t s = blockIdx.x;
+    const int64_t s = blockIdx.y;
     const int np = (a.P + kPT - 1) / kPT;
-    const int h = blockIdx.y / np, p0 = (blockIdx.y % np) * kPT;
+    const int h = blockIdx.x / np, p0 = (blockIdx.x % np) * kPT;
     const int g = h / (a.H / a.G);
     const int rows = min(kPT, a.P - p0);
     int64_t lo, hi;
@@ -535,7 +535,7 @@ template <int NV, int LR, int RL, Walk WALK>
 void recurrent(const RecArgs &r, cudaStream_t stream)
 {
     constexpr int rows = 128 / LR * RL;
-    const dim3 grid((unsigned)r.S, (unsigned)(r.H * ((r.P + rows - 1) / rows)));
+    const dim3 grid((unsigned)(r.H * ((r.P + rows - 1) / rows)), (unsigned)r.S);
     head_recurrent_kernel<NV, LR, RL, WALK><<<grid, 128, 0, stream>>>(r);
 }
 

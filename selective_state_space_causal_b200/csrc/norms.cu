@@ -513,7 +513,7 @@ cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int
     const bool warp = vec && nv <= 64;
     void (*kernel)(Args);
     int threads = 256;
-    if (!vec || nv > 1024) {
+    if (!vec || nv > 2048) {
         kernel = norm_bwd_any_kernel<T, R, MODE>;
     } else if (nv <= 32) {
         kernel = norm_bwd_kernel<T, R, MODE, true, 1, 256, 2>;
@@ -525,9 +525,12 @@ cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int
     } else if (nv <= 640) {
         kernel = norm_bwd_kernel<T, R, MODE, false, 2, 320, 2>;
         threads = (int)block_of(nv, 2);
-    } else {
+    } else if (nv <= 1024) {
         kernel = norm_bwd_kernel<T, R, MODE, false, 2, 512, 1>;
         threads = (int)block_of(nv, 2);
+    } else {
+        kernel = norm_bwd_kernel<T, R, MODE, false, 4, 512, 1>;
+        threads = (int)block_of(nv, 4);
     }
     // one wave of blocks over all groups, and no more partial rows than the workspace has
     int64_t blocks = warp ? (n.tok + 7) / 8 : n.tok, most = resident((const void *)kernel, threads) / groups;

@@ -141,3 +141,51 @@ def test_split_walks(S, tok):
             ho.close(g["du"][a:b], rdu.transpose(0, 1).cpu(), True, 1e-4, "du", size.transpose(0, 1).cpu())
             gs = torch.exp(c[:, -1])[:, None, None] * gs + (e * ya).transpose(1, 2) @ Cc[a:b]
         ho.close(g["dh0"][s], gs.cpu(), False, 1e-4, "dh0")
+
+
+def test_split_walks_with_the_state_in_place():
+    """h_final may be h0: every segment of a cut walk starts from h0, the last one ends in it.
+    Dense and packed, against the same call with its own h_final, bit for bit."""
+    tok, H, P, G, N = 8200, 2, 96, 1, 40
+    u, delta, A, B, C, D, bias = inputs(tok, H, P, G, N, BF, 9)
+    A = A * 0.02
+    for S, cu in ((1, None), (2, None), (3, torch.tensor([0, 7000, 7000, tok], dtype=torch.int32, device="cuda"))):
+        h0 = torch.randn((S, H, P, N), device="cuda")
+        y, hf = fwd(u, delta, A, B, C, D, bias, h0, cu, S)
+        y2, h2 = torch.empty_like(y), h0.clone()
+        n = ssm.ssm_head_scan_workspace_size(tok, H, P, G, N, S, BF)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        ssm.ssm_head_scan_fwd(u, delta, A, B, C, y2, Dskip=D, dt_bias=bias, h0=h2, h_final=h2, cu_seqlens=cu,
+                              S=S, workspace=ws)
+        assert torch.equal(y, y2) and torch.equal(hf, h2)
+        # and the 64-bit recurrence's end, a chunk at a time
+        f = lambda t: t.double()  # noqa: E731
+        d = ho.softplus(f(delta) + f(bias))
+        lens = [tok // S] * S if cu is None else (cu[1:] - cu[:-1]).tolist()
+        for s, (lo, hi) in enumerate(ho.bounds_of(lens)):
+            h = f(h0[s])
+            for a in range(lo, hi, 128):
+                b = min(a + 128, hi)
+                c = torch.cumsum(d[a:b] * f(A), 0).t()
+                w = d[a:b].t() * torch.exp(c[:, -1:] - c)
+                h = torch.exp(c[:, -1])[:, None, None] * h + (w[..., None] * f(u[a:b]).transpose(0, 1)).transpose(1, 2) @ f(B[a:b, 0])
+            ho.close(hf[s], h.cpu(), False, 1e-4, "h_final")
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_tens_of_thousands_of_heads(dt):
+    """As many heads as the checks allow, each with its own B and C, two tokens."""
+    tok, H, P, N = 2, 65535, 40, 3
+    u, delta, A, B, C, D, bias = inputs(tok, H, P, H, N, dt, 5)
+    dy = torch.randn(tok, H, P, device="cuda").to(dt)
+    y, hf = fwd(u, delta, A, B, C, D, bias, None, None, 1)
+    g = bwd(u, delta, A, B, C, D, bias, None, None, 1, dy)
+    f = lambda t: t.double().cpu()  # noqa: E731
+    a = [f(t) for t in (u, delta, A, B, C, D, bias)] + [True, None, [tok]]
+    ry, rh = ho.scan(*a)
+    rg = ho.scan_bwd(*a, f(dy), None)
+    size = ho.sizes(*a, f(dy), None) if dt == BF else {}
+    ho.close(y, ry, dt == BF, 1e-4, "y", size.get("y"))
+    ho.close(hf, rh, False, 1e-4, "h_final")
+    for k in ("du", "ddelta", "dB", "dC"):
+        ho.close(g[k], rg[k], dt == BF, 1e-4, k, size.get(k))

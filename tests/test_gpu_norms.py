@@ -205,3 +205,72 @@ def test_a_block_end_to_end(dt):
     for name, got in dict(x=dx, z=dz, B=gr["dB"], C=gr["dC"], delta=gr["ddelta"], res=dres, w1=dw1, w2=dw2,
                           Dk=gr["dDskip"], bias=gr["ddt_bias"], A=gr["dA"]).items():
         ho.close(got, rg[name], False, 3e-4, name)
+
+
+@pytest.mark.parametrize("dt,rdt", [(F32, F32), (BF, F32), (BF, BF)], ids=["f32", "bf16_f32", "bf16"])
+@pytest.mark.parametrize("D", [5120, 8192, 9000])
+def test_wide_rows(D, dt, rdt):
+    """Rows of more than 4096 columns, gate and stream, more rows than blocks."""
+    tok = 700
+    g = torch.Generator().manual_seed(D)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x, z, dy, ro, dro = r(tok, D).to(dt), r(tok, D).to(dt), r(tok, D).to(dt), r(tok, D).to(rdt), r(tok, D).to(rdt)
+    w = 1.0 + 0.3 * r(D)
+    gw = w.cuda()
+    gr = {"dx": torch.empty_like(x, device="cuda"), "dz": torch.empty_like(x, device="cuda"), "dweight": torch.empty_like(gw)}
+    ssm.ssm_gated_norm_bwd(x.cuda(), dy.cuda(), gr, weight=gw, z=z.cuda(), workspace=ws_of(tok, D))
+    lx, lz, lw = (t.double().requires_grad_() for t in (x, z, w))
+    ref = torch.autograd.grad(ho.norm(lx * torch.nn.functional.silu(lz), D, EPS) * lw, [lx, lz, lw], dy.double())
+    for k, v in zip(("dx", "dz", "dweight"), ref):
+        ho.close(gr[k], v, dt == BF and k != "dweight", 1e-4, k)
+    g2 = {"dresidual": torch.empty_like(ro, device="cuda"), "dweight": torch.empty_like(gw), "dx_scale": torch.empty_like(gw)}
+    ssm.ssm_residual_norm_bwd(ro.cuda(), dy.cuda(), g2, x=x.cuda(), weight=gw, alpha=0.5, dresidual_out=dro.cuda(),
+                              workspace=ws_of(tok, D))
+    lr, lw = ro.double().requires_grad_(), w.double().requires_grad_()
+    dr, dw = torch.autograd.grad(ho.norm(lr, D, EPS) * lw, [lr, lw], dy.double())
+    dr = dr + dro.double()
+    ho.close(g2["dresidual"], dr, rdt == BF, 1e-4, "dresidual")
+    ho.close(g2["dweight"], dw, False, 1e-4, "dweight")
+    ho.close(g2["dx_scale"], 0.5 * (dr * x.double()).sum(0), False, 1e-4, "dx_scale")
+
+
+def test_captured_and_on_another_stream():
+    """A block's norms, forward and backward, captured beside each other on a side stream
+    with a workspace each: replays give the eager results for inputs changed in place."""
+    tok, D = 300, 1536
+    side = torch.cuda.Stream()
+    runs = []
+    for i in range(2):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        x, z, dy = (torch.randn(tok, D, generator=g, device="cuda").to(BF) for _ in range(3))
+        res, w = torch.randn(tok, D, generator=g, device="cuda"), torch.rand(D, generator=g, device="cuda")
+        o = {k: torch.zeros_like(x) for k in ("y", "n", "dx", "dz")}
+        o.update(ro=torch.zeros_like(res), dweight=torch.zeros_like(w), dw2=torch.zeros_like(w))
+        ws = ws_of(tok, D)
+
+        def block(x=x, z=z, dy=dy, res=res, w=w, o=o, ws=ws):
+            ssm.ssm_residual_norm_fwd(x, o["n"], residual=res, residual_out=o["ro"], weight=w)
+            ssm.ssm_gated_norm_fwd(o["n"], o["y"], weight=w, z=z)
+            ssm.ssm_gated_norm_bwd(o["n"], dy, {"dx": o["dx"], "dz": o["dz"], "dweight": o["dweight"]}, weight=w,
+                                   z=z, workspace=ws)
+            ssm.ssm_residual_norm_bwd(o["ro"], o["dx"], {"dweight": o["dw2"]}, weight=w, workspace=ws)
+
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            block()
+        runs.append((graph, block, x, o))
+    for graph, block, x, o in runs:
+        x.mul_(0.5)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        runs[0][0].replay()
+    runs[1][0].replay()
+    torch.cuda.synchronize()
+    for graph, block, x, o in runs:
+        got = {k: v.clone() for k, v in o.items()}
+        block()
+        torch.cuda.synchronize()
+        for k, v in got.items():
+            assert torch.equal(v, o[k]), k
+            assert v.abs().sum() > 0
