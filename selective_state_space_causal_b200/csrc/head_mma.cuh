@@ -198,6 +198,27 @@ inline bool vec16(const void *p, int64_t stride, int64_t width)
 
 }  // namespace hm
 
+// How many of `units` (panels or heads) one CTA takes when `ctas` CTAs could take all of
+// theirs: the fewest whole waves over 148 SMs, a CTA's start counted as `start` units. At most
+// 16 waves are tried: a start is a small part of a CTA's time by then.
+inline int64_t units_of_cta(int64_t ctas, int64_t units, double start)
+{
+    int64_t best = units;
+    double cost = -1.0;
+    for (int64_t waves = 1; waves <= 16; ++waves) {
+        int64_t r = ctas > 0 ? waves * 148 / ctas : units;
+        r = r < 1 ? 1 : r > units ? units : r;
+        const int64_t per = (units + r - 1) / r, ranges = (units + per - 1) / per;
+        const double c = (double)((ctas * ranges + 147) / 148) * ((double)per + start);
+        if (cost < 0.0 || c < cost) {
+            cost = c;
+            best = per;
+        }
+        if (r == units) break;
+    }
+    return best;
+}
+
 // Sums of the chunks' shares (slot, head, 3) of dA, ddt_bias and dDskip, in a fixed order.
 cudaError_t launch_head_reduce(const float *part, int64_t slots, int H, float *dA, float *dbias,
                                float *dskip, cudaStream_t stream, int *launches);

@@ -820,12 +820,9 @@ BwdLayout bwd_layout(const Dims &z, bool known)
     l.walk = layout_of(z, 2, l.plan);
     const int64_t slots = head_slots(z.tok, z.S, kC);
     const size_t marks = l.walk.order - l.walk.marks;
-    // whole heads per CTA; G^T and the rounded dG^T are shared by a CTA's panels, so as few
-    // ranges as leave about three CTAs an SM
-    int64_t heads = z.H / z.G, per = slots * z.G * heads / (148 * 3);
-    per = per < 1 ? 1 : per > heads ? heads : per;
-    l.ranges = (int)((heads + per - 1) / per);
-    l.per = (int)((heads + l.ranges - 1) / l.ranges) * z.np;  // ranges of like size
+    // whole heads per CTA; G^T and the rounded dG^T are shared by a CTA's panels: a start and
+    // an end worth about two panels
+    l.per = (int)units_of_cta(slots * z.G, z.H / z.G, 2.0 / z.np) * z.np;
     l.ranges = (z.npan + l.per - 1) / l.per;
     l.dS = l.walk.total;
     l.dg = l.dS + marks;

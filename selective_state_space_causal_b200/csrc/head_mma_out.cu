@@ -343,12 +343,8 @@ cudaError_t launch_forward(const HeadScanArgs &a, cudaStream_t st, int *launches
     if (cudaError_t e = launch_states(s, false, 1, plan, vec, st, launches); e != cudaSuccess) return e;
     if (a.tok == 0) return cudaSuccess;
     const int64_t slots = head_slots(z.tok, z.S, kC);
-    // G is made once per CTA: as many panels a CTA as leave about four CTAs an SM
-    int64_t per = slots * z.G * z.npan / (148 * 4);
-    per = per < 2 ? 2 : per > 24 ? 24 : per;
-    if (per > z.npan) per = z.npan;
-    const int64_t ranges = (z.npan + per - 1) / per;
-    per = (z.npan + ranges - 1) / ranges;  // ranges of like size
+    // G is made once per CTA, a start worth about two panels
+    const int64_t per = units_of_cta(slots * z.G, z.npan, 2.0);
     OutArgs o{z, static_cast<const bf16 *>(a.u), static_cast<const bf16 *>(a.B), static_cast<const bf16 *>(a.C),
               a.u_stride, a.bc_stride, a.Dskip, tab, marks, static_cast<bf16 *>(a.y), (int)per, vec16(a.y, a.P, a.P)};
     ++*launches;
