@@ -30,6 +30,8 @@ __device__ int g_status;
 
 namespace {
 
+constexpr int kTabHeads = 8;
+
 // 2^x with the argument's rounding to fp32 made good: at x = -20 it alone is 1e-6.
 __device__ __forceinline__ float exp2_of(double x)
 {
@@ -37,7 +39,7 @@ __device__ __forceinline__ float exp2_of(double x)
     return fmaf(r, (float)(x - (double)h) * 0.6931471806f, r);
 }
 
-// One block per (chunk slot, 32 heads). Sums and their differences are 64-bit. Bound by
+// One block per (chunk slot, kTabHeads heads), a warp per head. Sums and their differences are 64-bit. Bound by
 // the latency of a block's few steps: 56 us for 65536 tokens of 80 heads (0.18 GB), 18 us
 // for 16384 of 24.
 __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *delta, int64_t stride,
@@ -45,9 +47,9 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
                                                          int softplus, bool backward, float *tab,
                                                          Plan plan, int64_t *span)
 {
-    __shared__ float sd[kC][33];
+    __shared__ float sd[kC][kTabHeads + 1];
     const int64_t slot = blockIdx.x;
-    const int h0 = blockIdx.y * 32, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int h0 = blockIdx.y * kTabHeads, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (plan.mode == Plan::kAsk && blockIdx.x + blockIdx.y == 0) {
         // the walks are cut only if the longest sequence would outlast two passes of pieces
         __shared__ int longest;
@@ -65,16 +67,16 @@ __global__ void __launch_bounds__(256) head_table_kernel(Dims z, const bf16 *del
     }
     const ChunkRef ck = find_chunk(z.cu, z.S, z.tok, kC, slot);
     if (ck.len == 0) return;
-    const int h = h0 + lane;
+    const int hl = tid % kTabHeads, h = h0 + hl;
     const float bs = bias && h < z.H ? bias[h] : 0.0f;
-#pragma unroll 4
-    for (int t = warp; t < kC; t += 8) {
+#pragma unroll
+    for (int t = tid / kTabHeads; t < kC; t += 256 / kTabHeads) {
         float v = 0.0f;
         if (t < ck.len && h < z.H) v = head_step(to_f32(delta[(ck.start + t) * stride + h]) + bs, softplus);
-        sd[t][lane] = v;
+        sd[t][hl] = v;
     }
     __syncthreads();
-    for (int i = warp; i < 32 && h0 + i < z.H; i += 8) {
+    for (int i = warp; i < kTabHeads && h0 + i < z.H; i += 8) {
         const float Ah = A[h0 + i];
         double run[4], sum = 0.0;
         float dv[4];
@@ -600,7 +602,7 @@ Plan plan_of(const Dims &z, bool known)
 cudaError_t launch_tables(const HeadScanArgs &a, const Dims &z, float *tab, bool backward,
                           const Plan &plan, int64_t *span, cudaStream_t stream, int *launches)
 {
-    const dim3 grid((unsigned)head_slots(z.tok, z.S, kC), (unsigned)((z.H + 31) / 32));
+    const dim3 grid((unsigned)head_slots(z.tok, z.S, kC), (unsigned)((z.H + kTabHeads - 1) / kTabHeads));
     head_table_kernel<<<grid, 256, 0, stream>>>(z, static_cast<const bf16 *>(a.delta), a.delta_stride,
                                                 a.A, a.dt_bias, a.delta_softplus, backward, tab,
                                                 plan, span);
