@@ -13,8 +13,8 @@
 // 32-token block i and s in an earlier one it is e^{c_t - r_i} e^{r_i - c_s}, r_i the
 // running sum before block i, and both factors are at most one.
 //
-// Measured on a B200, 65536 tokens, 80 heads of 64 x 128: 471 us for 2.15 GB (u, y, the
-// states before the chunks, tables), 4.6 TB/s or 70% of a copy's rate; 20% of the matrix
+// Measured on a B200, 65536 tokens, 80 heads of 64 x 128: 441 us for 2.15 GB (u, y, the
+// states before the chunks, tables), 4.9 TB/s or 75% of a copy's rate; 20% of the matrix
 // rate. Bound by a team's chain of waits (tables and u in, M, product, y out) at two teams
 // an SM, which shared memory allows. Roles instead of teams (16 warps for M, 8 for y) took
 // 548 us.
