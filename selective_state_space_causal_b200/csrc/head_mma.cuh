@@ -200,7 +200,9 @@ inline bool vec16(const void *p, int64_t stride, int64_t width)
 
 // How many of `units` (panels or heads) one CTA takes when `ctas` CTAs could take all of
 // theirs: the fewest whole waves over 148 SMs, a CTA's start counted as `start` units. At most
-// 16 waves are tried: a start is a small part of a CTA's time by then.
+// 16 waves are tried: a start is a small part of a CTA's time by then. Outputs of 136 chunks
+// of 24 panels: 39 us with all panels in a CTA, 58 with five; of 555 chunks of 80 panels 441
+// us with all, 471 with 20.
 inline int64_t units_of_cta(int64_t ctas, int64_t units, double start)
 {
     int64_t best = units;
