@@ -108,12 +108,27 @@ template <int COLS>
 __device__ __forceinline__ void load_tile_warp(uint32_t dst, const bf16 *src, int64_t stride, int len,
                                                int cols, int lane)
 {
-    constexpr int PIECES = COLS / 8;
-    for (int i = lane; i < kC * PIECES; i += 32) {
-        const int r = i / PIECES, c = i % PIECES, n = min(8, cols - 8 * c);
-        const bool in = r < len && n > 0;
-        sts16(dst + (c / 8) * umma::kPanel + umma::piece(r, c % 8),
-              in ? read8(src + r * stride + 8 * c, n) : make_uint4(0, 0, 0, 0));
+    constexpr int PIECES = COLS / 8, BATCH = 4;  // loads of a batch are all under way before a store
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src) | (uintptr_t)stride * 2;  // what all rows are aligned to
+    const int unit = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 2;
+    for (int i0 = lane; i0 < kC * PIECES; i0 += 32 * BATCH) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int r = (i0 + 32 * j) / PIECES, c = (i0 + 32 * j) % PIECES, n = min(8, cols - 8 * c);
+            const bf16 *q = src + r * stride + 8 * c;
+            if (r >= len || n <= 0) v[j] = make_uint4(0, 0, 0, 0);
+            else if (n == 8 && unit == 16) v[j] = *reinterpret_cast<const uint4 *>(q);
+            else if (n == 8 && unit == 4) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
+                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            } else v[j] = read8(q, n);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int r = (i0 + 32 * j) / PIECES, c = (i0 + 32 * j) % PIECES;
+            sts16(dst + (c / 8) * umma::kPanel + umma::piece(r, c % 8), v[j]);
+        }
     }
 }
 
