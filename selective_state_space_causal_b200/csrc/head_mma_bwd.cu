@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
         for (int i = 0; i < 2; ++i) {
             mbar_init_n(&ud[i], 1);
             mbar_init_n(&epi[i], kWork);
-            mbar_init_n(&fin[i], 1);
+            mbar_init_n(&fin[i], kFinish);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -263,14 +263,22 @@ __global__ void __launch_bounds__(kBwdThreads) head_bwd_kernel(BwdArgs a, const 
         __syncwarp();
     } else if (warp >= kBFinish) {
         // two warps, heads in turn: tokens 4 lane .. 4 lane + 3, sums over a head's panels,
-        // then the head's gradients
+        // then the head's gradients. A barrier tells phases apart by parity only, so a warp
+        // may skip none of a buffer's: both wait for every panel's sums and free them,
+        // whichever of them reads them. (Heads of one panel could do without, as a warp's
+        // panels are then all those of one buffer: 1565 us instead of 1569 for a whole call.)
         float R[4], K[4], I[4], J[4], own[4], dsk = 0.0f, dot = 0.0f;
         auto add4 = [&](float (&v)[4], const float *q) {
             const float4 x = *reinterpret_cast<const float4 *>(q + 4 * lane);
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
         };
         for (int it = 0; it < count; ++it) {
-            if (it / z.np % kFinish != warp - kBFinish) continue;
+            if (it / z.np % kFinish != warp - kBFinish) {  // the other warp's head
+                wait(&epi[it & 1], it >> 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&fin[it & 1]);
+                continue;
+            }
             const PanelRef p = panel_of(z, g, pb + it);
             const bool start = p.p0 == 0, end = p.p0 + 64 >= z.P;
             const float *tb = a.tab + (slot * z.H + p.h) * kTab;
