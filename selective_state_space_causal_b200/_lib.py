@@ -427,6 +427,24 @@ def _same(what: str, t, dtype, shape) -> None:
                            f"got {t.dtype} {tuple(t.shape)}")
 
 
+def _sequences(cu_seqlens, S) -> int:
+    """S, after checking that cu_seqlens (int32) holds S + 1 offsets or more; of a None, the
+    sequences of cu_seqlens, or one."""
+    import torch
+
+    if cu_seqlens is None:
+        return 1 if S is None else S
+    n = cu_seqlens.numel() - 1
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        raise SsmError(-1, f"cu_seqlens: expected a contiguous vector of {torch.int32}, got "
+                           f"{cu_seqlens.dtype} {tuple(cu_seqlens.shape)}")
+    if S is None:
+        S = n
+    elif S > n:
+        raise SsmError(-1, f"cu_seqlens has {n + 1} offsets, {S} sequences need {S + 1}")
+    return S
+
+
 def _head_shapes(u, delta, A, B, C, Dskip, dt_bias):
     """(tok, H, P, G, N) after checking that the arguments agree."""
     import torch
@@ -485,13 +503,13 @@ def ssm_head_scan_fwd(u, delta, A, B, C, y, Dskip=None, dt_bias=None, delta_soft
                       h0=None, h_final=None, cu_seqlens=None, S=None, workspace=None, stream=None):
     """Scan with one decay per head. u (tok, H, P), delta (tok, H) and B, C (tok, G, N)
     may be slices of wider rows (tokens contiguous); y (tok, H, P) contiguous; A, Dskip,
-    dt_bias (H) fp32; h0, h_final (S, H, P, N) fp32; workspace: a device byte tensor of
-    ssm_head_scan_workspace_size() bytes."""
+    dt_bias (H) fp32; h0, h_final (S, H, P, N) fp32; cu_seqlens int32, S + 1 offsets (more
+    where S is given); workspace: a device byte tensor of ssm_head_scan_workspace_size()
+    bytes."""
     import torch
 
     tok, H, P, G, N = _head_shapes(u, delta, A, B, C, Dskip, dt_bias)
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     _same("y", y, u.dtype, (tok, H, P))
     _same("h0", h0, torch.float32, (S, H, P, N))
     _same("h_final", h_final, torch.float32, (S, H, P, N))
@@ -517,8 +535,7 @@ def ssm_head_scan_bwd(u, delta, A, B, C, dy, grads, Dskip=None, dt_bias=None, de
     import torch
 
     tok, H, P, G, N = _head_shapes(u, delta, A, B, C, Dskip, dt_bias)
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     g, f32 = grads, torch.float32
     _same("h0", h0, f32, (S, H, P, N))
     _same("dh_final", dh_final, f32, (S, H, P, N))
