@@ -193,6 +193,26 @@ def ssm_check_cu_seqlens(cu_seqlens_host, tok: int) -> None:
     _check(lib.ssm_check_cu_seqlens(_ptr(cu_seqlens_host), S, int(tok)))
 
 
+def _sequences(cu_seqlens, S) -> int:
+    """S, after checking that cu_seqlens (int32) holds S + 1 offsets or more; of a None, the
+    sequences of cu_seqlens, or one. An address says nothing of what it holds."""
+    if cu_seqlens is None:
+        return 1 if S is None else S
+    if S is not None and isinstance(cu_seqlens, int):
+        return S
+    import torch
+
+    n = cu_seqlens.numel() - 1
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+        raise SsmError(-1, f"cu_seqlens: expected contiguous {torch.int32}, got {cu_seqlens.dtype} "
+                           f"{tuple(cu_seqlens.shape)}")
+    if S is None:
+        S = n
+    elif S > n:
+        raise SsmError(-1, f"cu_seqlens has {n + 1} offsets, {S} sequences need {S + 1}")
+    return S
+
+
 def ssm_scan_workspace_size(tok: int, D: int, N: int, S: int) -> int:
     return int(lib.ssm_scan_workspace_size(tok, D, N, S))
 
@@ -202,8 +222,7 @@ def ssm_causal_conv1d(x, xc, weight, bias=None, cu_seqlens=None, S=None, conv_st
     """x, xc: (tok, D); weight (D, K) fp32; states (S, D, K-1)."""
     tok, D = x.shape
     K = weight.shape[1]
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     st = conv_state_in if conv_state_in is not None else conv_state_out
     sdt = _dtype(st) if st is not None else _dtype(x)
     _check(lib.ssm_causal_conv1d(_ptr(x), _ptr(xc), _ptr(weight), _ptr(bias), tok, D, K,
@@ -217,8 +236,7 @@ def ssm_selective_scan_fwd(u, delta, A, B, C, y, Dskip=None, z=None, dt_bias=Non
     """u, delta, z, y: (tok, D); A (D, N); B, C (tok, N); h0 / h_final (S, D, N) fp32."""
     tok, D = u.shape
     N = A.shape[1]
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ssm_selective_scan_fwd(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                                       _ptr(Dskip), _ptr(z), _ptr(dt_bias), int(bool(delta_softplus)),
@@ -234,8 +252,7 @@ def ssm_selective_scan_fwd_ckpt(u, delta, A, B, C, y, bwd_workspace, Dskip=None,
     that ssm_selective_scan_bwd_ckpt reads instead of recomputing them."""
     tok, D = u.shape
     N = A.shape[1]
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     bws_bytes = 0 if bwd_workspace is None else bwd_workspace.numel() * bwd_workspace.element_size()
     _check(lib.ssm_selective_scan_fwd_ckpt(
@@ -255,8 +272,7 @@ def ssm_selective_scan_fwd_noalloc(u, delta, A, B, C, y, Dskip=None, z=None, dt_
     calls on one GPU share the scratch and race."""
     tok, D = u.shape
     N = A.shape[1]
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     _check(lib.ssm_selective_scan_fwd_noalloc(
         _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(dt_bias),
         int(bool(delta_softplus)), _ptr(h0), _ptr(cu_seqlens), S, _ptr(y), _ptr(h_final), tok, D,
@@ -362,8 +378,7 @@ def ssm_selective_scan_bwd(u, delta, A, B, C, dy, grads, Dskip=None, z=None, dt_
     (ssm_selective_scan_bwd_ckpt)."""
     tok, D = u.shape
     N = A.shape[1]
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     g = grads
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     fn = lib.ssm_selective_scan_bwd_ckpt if from_fwd_ckpt else lib.ssm_selective_scan_bwd
@@ -384,8 +399,7 @@ def ssm_conv_scan_fwd(x, conv_w, delta, A, B, C, y, conv_b=None, conv_state_in=N
     tok, D = x.shape
     N = A.shape[1]
     K = conv_w.shape[1]
-    if S is None:
-        S = (cu_seqlens.numel() - 1) if cu_seqlens is not None else 1
+    S = _sequences(cu_seqlens, S)
     st = conv_state_in if conv_state_in is not None else conv_state_out
     sdt = _dtype(st) if st is not None else _dtype(x)
     _check(lib.ssm_conv_scan_fwd(
@@ -425,24 +439,6 @@ def _same(what: str, t, dtype, shape) -> None:
     if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
         raise SsmError(-1, f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
                            f"got {t.dtype} {tuple(t.shape)}")
-
-
-def _sequences(cu_seqlens, S) -> int:
-    """S, after checking that cu_seqlens (int32) holds S + 1 offsets or more; of a None, the
-    sequences of cu_seqlens, or one."""
-    import torch
-
-    if cu_seqlens is None:
-        return 1 if S is None else S
-    n = cu_seqlens.numel() - 1
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
-        raise SsmError(-1, f"cu_seqlens: expected a contiguous vector of {torch.int32}, got "
-                           f"{cu_seqlens.dtype} {tuple(cu_seqlens.shape)}")
-    if S is None:
-        S = n
-    elif S > n:
-        raise SsmError(-1, f"cu_seqlens has {n + 1} offsets, {S} sequences need {S + 1}")
-    return S
 
 
 def _head_shapes(u, delta, A, B, C, Dskip, dt_bias):
