@@ -563,9 +563,9 @@ int ssm_selective_scan_fwd_noalloc(const void *u, const void *delta, const float
  *   workspace      >= ssm_head_scan_workspace_size() bytes, 256-byte aligned
  *                  (NULL where that is 0); overwritten. Calls that may run at the
  *                  same time (streams, captured graphs) need one each
- * y must not overlap an input. Any alignment is taken; rows of bf16 that are all
- * 16-byte aligned load faster. A decay below exp(-208) is taken as exp(-208),
- * which is 0 in fp32. Inside one sequence a NaN or infinity in u, B, C or delta
+ * y, h_final (but for h0) and the workspace must not overlap an input or one another.
+ * Any alignment is taken; rows of bf16 that are all 16-byte aligned load faster. A
+ * decay below exp(-208) is taken as exp(-208), which is 0 in fp32. Inside one sequence a NaN or infinity in u, B, C or delta
  * may reach every output of its own 128-token chunk, the tokens before it
  * included, and all outputs after it; it never reaches another sequence.
  * bf16: the products run on the tensor cores; the state, the decays and every sum

@@ -864,13 +864,13 @@ int ssm_head_scan_fwd(const void *u, int64_t u_stride, const void *delta, int64_
     if (int r = check_workspace(fn, workspace, workspace_bytes, need)) return r;
     const size_t es = esize(act_dtype), bc = span_bytes(tok, bc_stride, G * N, es);
     const size_t state = (size_t)S * H * P * N * 4;
-    const Region outs[] = {{y, (size_t)tok * H * P * es}, {workspace, need}};
+    const size_t heads = (size_t)H * 4, offsets = (size_t)(S + 1) * 4;
+    const Region outs[] = {{y, (size_t)tok * H * P * es}, {h_final, state}, {workspace, need}};
     const Region ins[] = {{u, span_bytes(tok, u_stride, H * P, es)},
                           {delta, span_bytes(tok, delta_stride, H, es)}, {B, bc}, {C, bc},
-                          {h0, state}, {h_final, state}};
+                          {h_final == h0 ? nullptr : h0, state}, {A, heads}, {Dskip, heads},
+                          {dt_bias, heads}, {cu_seqlens, offsets}};
     if (int r = check_apart(fn, outs, ins)) return r;
-    if (h_final != h0 && overlap(h_final, state, h0, state))
-        return fail(SSM_ERR_INVALID_ARGUMENT, "%s: h_final overlaps h0 without being it", fn);
     int launched = 0;
     cudaError_t e = ssm::launch_head_scan(a, reinterpret_cast<cudaStream_t>(stream), &launched);
     return finish(e, launched, fn);
@@ -906,7 +906,7 @@ int ssm_head_scan_bwd(const void *u, int64_t u_stride, const void *delta, int64_
     const Region ins[] = {{u, span_bytes(tok, u_stride, H * P, es)},
                           {delta, span_bytes(tok, delta_stride, H, es)}, {B, bc}, {C, bc},
                           {dy, rows}, {h0, state}, {dh_final, state}, {A, heads},
-                          {Dskip, heads}, {dt_bias, heads}};
+                          {Dskip, heads}, {dt_bias, heads}, {cu_seqlens, (size_t)(S + 1) * 4}};
     if (int r = check_apart(fn, outs, ins)) return r;
     int launched = 0;
     cudaError_t e = ssm::launch_head_scan_bwd(a, reinterpret_cast<cudaStream_t>(stream), &launched);
@@ -944,7 +944,9 @@ int ssm_head_state_update(float *ssm_state, const void *x, int64_t x_stride, con
     const size_t bc = span_bytes(Bt, bc_stride, G * N, es);
     const Region outs[] = {{y, (size_t)Bt * H * P * es}};
     const Region ins[] = {{x, span_bytes(Bt, x_stride, H * P, es)},
-                          {dt_, span_bytes(Bt, dt_stride, H, es)}, {B, bc}, {C, bc}};
+                          {dt_, span_bytes(Bt, dt_stride, H, es)}, {B, bc}, {C, bc},
+                          {A, (size_t)H * 4}, {Dskip, (size_t)H * 4}, {dt_bias, (size_t)H * 4},
+                          {state_indices, (size_t)Bt * 4}};
     if (int r = check_apart(fn, outs, ins)) return r;
     ssm::HeadStepArgs a{ssm_state, x, dt_, B, C, x_stride, dt_stride, bc_stride, A, Dskip, dt_bias,
                         delta_softplus, state_indices, n_slots, y, Bt, H, P, G, N, dt(act_dtype)};
