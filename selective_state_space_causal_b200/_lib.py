@@ -193,6 +193,16 @@ def ssm_check_cu_seqlens(cu_seqlens_host, tok: int) -> None:
     _check(lib.ssm_check_cu_seqlens(_ptr(cu_seqlens_host), S, int(tok)))
 
 
+def _bytes(workspace) -> int:
+    """Bytes of a workspace, which has to lie in one piece: a view that repeats or skips
+    memory has other bytes than its elements add up to."""
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise SsmError(-5, "a workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _sequences(cu_seqlens, S) -> int:
     """S, after checking that cu_seqlens (int32) holds S + 1 offsets or more; of a None, the
     sequences of cu_seqlens, or one. An address says nothing of what it holds."""
@@ -237,11 +247,11 @@ def ssm_selective_scan_fwd(u, delta, A, B, C, y, Dskip=None, z=None, dt_bias=Non
     tok, D = u.shape
     N = A.shape[1]
     S = _sequences(cu_seqlens, S)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.ssm_selective_scan_fwd(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                                       _ptr(Dskip), _ptr(z), _ptr(dt_bias), int(bool(delta_softplus)),
                                       _ptr(h0), _ptr(cu_seqlens), S, _ptr(y), _ptr(h_final), tok, D,
-                                      N, _dtype(u), _ptr(workspace), ws_bytes, _stream(stream)))
+                                      N, _dtype(u), _ptr(workspace), _bytes(workspace),
+                                      _stream(stream)))
 
 
 def ssm_selective_scan_fwd_ckpt(u, delta, A, B, C, y, bwd_workspace, Dskip=None, z=None,
@@ -253,12 +263,11 @@ def ssm_selective_scan_fwd_ckpt(u, delta, A, B, C, y, bwd_workspace, Dskip=None,
     tok, D = u.shape
     N = A.shape[1]
     S = _sequences(cu_seqlens, S)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    bws_bytes = 0 if bwd_workspace is None else bwd_workspace.numel() * bwd_workspace.element_size()
     _check(lib.ssm_selective_scan_fwd_ckpt(
         _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(dt_bias),
         int(bool(delta_softplus)), _ptr(h0), _ptr(cu_seqlens), S, _ptr(y), _ptr(h_final), tok, D,
-        N, _dtype(u), _ptr(workspace), ws_bytes, _ptr(bwd_workspace), bws_bytes, _stream(stream)))
+        N, _dtype(u), _ptr(workspace), _bytes(workspace), _ptr(bwd_workspace),
+        _bytes(bwd_workspace), _stream(stream)))
 
 
 def ssm_selective_scan_fwd_noalloc(u, delta, A, B, C, y, Dskip=None, z=None, dt_bias=None,
@@ -380,14 +389,13 @@ def ssm_selective_scan_bwd(u, delta, A, B, C, dy, grads, Dskip=None, z=None, dt_
     N = A.shape[1]
     S = _sequences(cu_seqlens, S)
     g = grads
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     fn = lib.ssm_selective_scan_bwd_ckpt if from_fwd_ckpt else lib.ssm_selective_scan_bwd
     _check(fn(
         _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(z), _ptr(dt_bias),
         int(bool(delta_softplus)), _ptr(h0), _ptr(cu_seqlens), S, _ptr(dy), _ptr(dh_final),
         _ptr(g["du"]), _ptr(g["ddelta"]), _ptr(g.get("dz")), _ptr(g["dB"]), _ptr(g["dC"]),
         _ptr(g["dA"]), _ptr(g.get("dDskip")), _ptr(g.get("ddt_bias")), _ptr(g.get("dh0")), tok, D,
-        N, _dtype(u), _ptr(workspace), ws_bytes, _stream(stream)))
+        N, _dtype(u), _ptr(workspace), _bytes(workspace), _stream(stream)))
 
 
 def ssm_conv_scan_fwd(x, conv_w, delta, A, B, C, y, conv_b=None, conv_state_in=None,
@@ -484,10 +492,6 @@ def _on_gpu(*tensors) -> None:
             if here is not None or d < 0 or d != torch.cuda.current_device():
                 raise SsmError(-1, f"a tensor is on {t.device}, not on the current CUDA device")
             here = d
-
-
-def _bytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
 
 
 def ssm_head_scan_workspace_size(tok: int, H: int, P: int, G: int, N: int, S: int, dtype) -> int:

@@ -95,3 +95,28 @@ def test_channel_calls_refuse_cu_seqlens(no_launch, name, kw):
 def test_channel_calls_take_good_sequences(no_launch, name, kw, S):
     channel_call(name, **kw)
     assert S in no_launch.got
+
+
+BYTES = z(64, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("ws", [BYTES[:1].expand(1 << 30), BYTES[::2]], ids=["repeats", "skips"])
+@pytest.mark.parametrize("name", ["fwd", "ckpt", "bwd", "head_fwd", "head_bwd", "gated", "residual"])
+def test_workspaces_in_one_piece(no_launch, monkeypatch, name, ws):
+    """A view's elements are not the bytes that lie behind its address."""
+    from selective_state_space_causal_b200 import _lib
+
+    monkeypatch.setattr(_lib, "_on_gpu", lambda *t: None)
+    with pytest.raises(ssm.SsmError, match="contiguous"):
+        if name.startswith("head"):
+            head_scan(name[5:], workspace=ws)
+        elif name == "gated":
+            ssm.ssm_gated_norm_bwd(z(4, 8), z(4, 8), {"dx": z(4, 8), "dweight": z(8)}, workspace=ws, stream=0)
+        elif name == "residual":
+            ssm.ssm_residual_norm_bwd(z(4, 8), z(4, 8), {"dweight": z(8)}, workspace=ws, stream=0)
+        else:
+            channel_call(name, workspace=ws)
+    if name == "ckpt":
+        with pytest.raises(ssm.SsmError, match="contiguous"):
+            a = z(6, 8), z(6, 8), z(8, 16), z(6, 16), z(6, 16), z(6, 8)
+            ssm.ssm_selective_scan_fwd_ckpt(*a, ws, stream=0)
