@@ -114,7 +114,7 @@ def _check(code: int) -> None:
 
 
 def _ptr(t):
-    if t is None or t.__class__ is int:
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 

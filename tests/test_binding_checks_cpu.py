@@ -120,3 +120,13 @@ def test_workspaces_in_one_piece(no_launch, monkeypatch, name, ws):
         with pytest.raises(ssm.SsmError, match="contiguous"):
             a = z(6, 8), z(6, 8), z(8, 16), z(6, 16), z(6, 16), z(6, 8)
             ssm.ssm_selective_scan_fwd_ckpt(*a, ws, stream=0)
+
+
+def test_addresses_of_an_int_subclass():
+    class Address(int):
+        pass
+
+    from selective_state_space_causal_b200._lib import _ptr
+
+    assert _ptr(Address(64)) == 64 and _ptr(64) == 64 and _ptr(None) is None
+    assert _ptr(BYTES) == BYTES.data_ptr()
