@@ -568,8 +568,13 @@ int ssm_selective_scan_fwd_noalloc(const void *u, const void *delta, const float
  * decay below exp(-208) is taken as exp(-208), which is 0 in fp32. Inside one sequence a NaN or infinity in u, B, C or delta
  * may reach every output of its own 128-token chunk, the tokens before it
  * included, and all outputs after it; it never reaches another sequence.
- * bf16: the products run on the tensor cores; the state, the decays and every sum
- * are fp32.
+ * bf16: the products run on the tensor cores. The state that is carried from token to
+ * token, h_final, the decays and every sum are fp32, but one factor of each product of y
+ * is rounded to bf16: inside a 128-token chunk the weight (C_t . B_s) decay d_s, across
+ * chunks the state that the chunk starts from. So y is off by at most 2^-8 of the sum of
+ * the sizes of its terms, beside the half step of its own type. Where the state grows
+ * (d A > 0), the decay between two tokens of a chunk is a product of two factors, split
+ * at a multiple of 32 tokens, and both have to stay below 2^127.
  */
 size_t ssm_head_scan_workspace_size(int64_t tok, int64_t H, int64_t P, int64_t G, int64_t N,
                                     int64_t S, ssm_dtype act_dtype);
@@ -589,7 +594,13 @@ int ssm_head_scan_fwd(const void *u, int64_t u_stride, const void *delta, int64_
  *   dd_t = u_t . g_t B_t + A <g_t, exp(d_t A) S_{t-1}>,  ddelta_t = dd_t softplus'
  *   dA = sum_t d_t <g_t, exp(d_t A) S_{t-1}>,  dDskip = sum dy . u,  ddt_bias = sum ddelta
  *   dh0 = exp(d_{t0} A) g_{t0} (first token t0; dh_final for an empty sequence)
- * The forward's states are recomputed.
+ * The forward's states are recomputed. Inside one sequence a NaN or infinity may reach
+ * all its gradients (and dA, dDskip, ddt_bias of its heads), never another sequence's.
+ * bf16, beside the rounding of what is stored: du takes a chunk's weights as bf16; dB
+ * and dC take the states before the chunks, and their gradients, as bf16, and what
+ * passes between two tokens of a chunk with 16 bits; ddelta, dA and ddt_bias take the
+ * states with 16 bits and unrounded weights, so dA and ddt_bias are off by a few 1e-6 of
+ * their size. dh0 and dDskip are as accurate as in fp32.
  *   the forward's arguments, unchanged, then
  *   dy             (tok, H, P) act_dtype, contiguous
  *   dh_final       (S, H, P, N) fp32 or NULL (= 0)
@@ -653,7 +664,8 @@ typedef struct {
  *   dweight        (D) fp32 or NULL, summed over rows in a fixed order
  *   workspace      >= ssm_norm_bwd_workspace_size(tok, D) bytes, 256-byte aligned;
  *                  needed when dweight (or dx_scale, below) is given
- * Norms and sums are fp32. D / group_size <= 65535.
+ * Norms and sums are fp32. For bf16 the gate is made with CUDA's faster exponential and
+ * division (some |z| fp32 ulps, below a bf16 step). D / group_size <= 65535.
  */
 size_t ssm_norm_bwd_workspace_size(int64_t tok, int64_t D);
 int ssm_gated_norm_fwd(const void *x, int64_t x_stride, const void *z, int64_t z_stride,

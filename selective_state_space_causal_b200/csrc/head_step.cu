@@ -5,8 +5,8 @@
 // Bound by memory: the state is read and written once, 8 bytes per entry, against
 // five flops. One CTA has one row's head; LR lanes share a state row (4 entries
 // each), and a lane issues the loads of up to 8 state rows before it uses the first.
-// Measured on a B200: 256 rows of 128 heads of 64 x 128 (2.15 GB) 360 us, 6.0 TB/s or 91%
-// of a copy's rate; one row of 24 heads 5 us, a launch's latency.
+// Measured on a B200: 256 rows of 128 heads of 64 x 128 (2.15 GB) 365 us, 5.9 TB/s or 90%
+// of a copy's rate (382 us from call to call); one row of 24 heads 5 us, a launch's latency.
 #include "head_scan.cuh"
 
 namespace ssm {

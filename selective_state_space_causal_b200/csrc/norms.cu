@@ -12,13 +12,15 @@
 // the row beyond) keeps its row in registers between the sums and the scaling. The
 // backward keeps the row as it was loaded, computes from it twice, and loads the next
 // row before it waits for this one's sums; the weights and their gradients' sums stay in
-// registers over all rows of a block (weights read per row: 244 us for the first line
+// registers over all rows of a block (weights read per row: 5% slower in the first line
 // below). Rows that are not 16-byte aligned, or longer than the registers hold, go to
 // kernels that read the row twice (the second time from cache).
 //
-// Measured on a B200, bf16, 16384 rows, of a copy's 6534 GB/s:
-//   gate then norm, 5120 wide      forward 100 us (5.0 TB/s, 77%), backward 232 us (3.6 TB/s, 55%)
-//   residual in fp32, 2560 wide    forward  79 us (6.4 TB/s, 97%), backward 152 us (4.4 TB/s, 67%)
+// Measured on a B200, bf16, 16384 rows, of a copy's 6534 GB/s (the weight gradients' sum over
+// partial rows takes 7 us more):
+//   gate then norm, 5120 wide      forward 102 us (4.9 TB/s, 76%), backward 235 us (3.6 TB/s, 55%)
+//   residual in fp32, 2560 wide    forward  81 us (6.2 TB/s, 95%), backward 152 us (5.0 TB/s, 76%, with
+//                                  a learned scale)
 // The forward with a gate and both backwards are held by what a row waits for: its loads,
 // one sum over the block, its stores, with 20 warps an SM in flight (registers), and by
 // the exponentials and reciprocals of the gate, taken twice an element in the backward.
@@ -504,6 +506,21 @@ int resident(const void *kernel, int threads)
     return per * sms;
 }
 
+// What a block is, by the vectors of a row (or group). To 320 one a thread and three blocks an
+// SM, to 640 two and two blocks, to 1024 two in a block of 512, then four. Backward of 16384 rows
+// in us, the weights' sum with it, as chosen and with the next size of thread or block:
+//   gated bf16     1024 wide 57 (two a thread, blocks to 320: 62; to 512: 55), 2560 133 (125; 125),
+//                  4096 209 (one a thread, blocks to 512: 197; two, to 512: 182), 5120 240 (two, to
+//                  512: 338), 6144 340 (four: 553), 8192 391 (594), 16384 1217
+//   gated fp32     1024 86 (two, to 512: 94), 2048 188 (182), 4096 397 (465), 8192 958
+//   fp32 stream    1024 68 (63; 66), 1280 92 (80; 88), 2048 133 (127), 2560 156 (238), 4096 281
+//                  (440), 8192 942
+// The steps at 640 and 1024 are worth a third; inside the first two ranges the neighbours are
+// within 15%, to either side. Four vectors a thread run out of registers: 3.0 times the bytes'
+// time where the others take 1.5 to 2.2.
+// With a warp a row (to 64 vectors) each warp has a partial row, so kParts allows one block of
+// eight warps an SM: 131072 rows of 512 182 us (bytes 103), of 256 105 (51). A group of 64
+// columns has work for 8 of a warp's 32 lanes: 16384 x 5120 in groups of 64 821 us (bytes 128).
 template <typename T, typename R, int MODE>
 cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int *parts)
 {
@@ -532,7 +549,7 @@ cudaError_t bwd(const NormArgs &n, const Args &a, bool vec, cudaStream_t st, int
         kernel = norm_bwd_kernel<T, R, MODE, false, 4, 512, 1>;
         threads = (int)block_of(nv, 4);
     }
-    // one wave of blocks over all groups, and no more partial rows than the workspace has
+    // at most one wave of blocks over all groups, and no more partial rows than the workspace has
     int64_t blocks = warp ? (n.tok + 7) / 8 : n.tok, most = resident((const void *)kernel, threads) / groups;
     if (most > kParts / (warp ? 8 : 1)) most = kParts / (warp ? 8 : 1);
     if (most < 1) most = 1;

@@ -125,7 +125,7 @@ __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.
 
 // mbar_wait for barriers that matrix instructions complete: these waits are short and
 // on the critical path, so they poll with the hardware's own suspend time. At most 2^22
-// tries, then bit 1 of *status is set and each later wait of this thread tries once. The
+// tries, then bit 0 of *status is set and each later wait of this thread tries once. The
 // count of tries is hidden from the compiler, which otherwise makes a second copy of
 // the code behind a wait for the case that it failed: the instruction cache feels it.
 constexpr unsigned kTries = 1u << 22;
